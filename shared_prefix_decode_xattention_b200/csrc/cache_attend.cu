@@ -1,0 +1,663 @@
+// cache_attend.cu -- attention over the paged 8-bit cache for rows with few
+// query rows (a decode step's single tokens, a few speculated ones, small
+// beams), and the join of partial results.
+//
+// Mathematics: with codes k_j, v_j, scales a_j, b_j (one for each page and kv
+// head) the scores are x_j = (q . k_j) a_j scale (capped, biased), the output
+// sum_j w_j v_j / l with w_j = 2^(x_j log2 e - m) b_j and l = sum_j 2^(x_j log2 e - m):
+// the scales leave the products, so the tensor cores multiply the codes
+// themselves.  Every 8-bit code is an fp16 number, and a bf16 query row is one
+// but for a power of two (2^e of its largest element, put back on the scores;
+// elements below 2^-17 of the row's largest lose bits, less than 2^-25 of it
+// absolute), so no product is rounded; sums, maxima and l are fp32.  The weights
+// are rounded to fp16 (2^-11 relative, finer than the bf16 of the output).  b_j
+// is taken relative to the largest b so far, as m is for x, so weights stay
+// within fp16's range whatever the scales.
+//
+// Layout: bound by streaming the codes from HBM.  A warp takes 32 keys at a
+// time through a ring of its own in shared memory (cp.async, 16 bytes a lane,
+// zero-filled behind the row's end), and multiplies with mma.sync m16n8k16: few
+// query rows (16 or 32 a tile) would leave a 128-row tcgen05 tile empty.  The
+// rows of a tile share one pass over the keys and one conversion of the codes.
+// The contraction index of a product may be permuted freely, so a lane's
+// fragment of K is 16 consecutive bytes of one key and of V 16 consecutive
+// dims of four keys: conversion needs no shuffles, the weights' fragments are
+// the scores' own registers, and all shared-memory reads are 16 bytes wide and
+// free of bank conflicts (perm and swz below).
+#include "cache_plan.cuh"
+
+namespace xgr {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kStages = 2;
+constexpr int kTileKeys = 32;
+
+// n index (0..7) of a fragment -> key within a group of 8
+template <int D>
+__device__ __forceinline__ constexpr int perm(int g) {
+    return D == 128 ? ((g & 1) << 2) | (g >> 1) : g ^ ((g >> 1) & 1);
+}
+// 16-byte chunk c of key `key` is stored at chunk c ^ swz(key)
+template <int D>
+__device__ __forceinline__ constexpr int swz(int key) {
+    return D == 128 ? key & 7 : ((key >> 2) & 1) << 1;
+}
+
+template <int D, int MT>
+struct Smem {
+    static constexpr int kStageBytes = kTileKeys * D * 2;      // K then V
+    alignas(16) uint8_t ring[kWarps][kStages][kStageBytes];    // after the loop: O [kWarps][R][D] fp32
+    alignas(16) float sc[kWarps][kStages][4];                  // K, K, V, V scales of the two 16-key halves
+    int bad[kWarps][kStages];                                  // bit h: half h lies in a page that is not there
+    float m[kWarps][16 * MT], l[kWarps][16 * MT];
+    float vref[kWarps];
+    alignas(16) uint32_t qf[MT > 1 ? MT * (D / 16) * 128 : 4];  // query fragments (MT > 1; else in registers)
+    static_assert(16 * MT * D * 4 <= kStages * kStageBytes, "the O buffer fits the rings");
+};
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the four codes of a word -> two fp16 pairs (elements 0, 1 and 2, 3)
+template <int FMT>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (FMT == XGR_CACHE_E4M3) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    } else {   // 1024 + (code + 128) is an fp16 number with the byte as its low bits
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
+        const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&l), off);
+        const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&h), off);
+        lo = *reinterpret_cast<const uint32_t *>(&a);
+        hi = *reinterpret_cast<const uint32_t *>(&b);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int D, int FMT, int MT>
+__global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel(AttendArgs a, RowsOf w, PlanOut po,
+                                                                              int min_units) {
+    constexpr int R = 16 * MT;
+    constexpr int KS = D / 16;                 // k steps of Q K^T
+    constexpr int NT = D / 8;                  // n tiles of P V
+    constexpr int kChunks = D / 16;            // 16-byte chunks of a key
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Smem<D, MT> &sm = *reinterpret_cast<Smem<D, MT> *>(smem_raw);
+    const CacheArgs &c = a.c;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int qr = lane / 4, qc = lane % 4;    // fragment row and column group
+
+    griddep_wait();
+    griddep_launch_dependents();
+    Cursor cur;
+    int64_t begin, end, per;
+    if (!plan_begin<kThreads>(a, w, min_units, po, cur, begin, end, per)) return;
+
+    const uint32_t ring0 = smem_u32(&sm.ring[warp][0][0]);
+    const uint32_t sc0 = smem_u32(&sm.sc[warp][0][0]);
+
+    for (int64_t at = begin; at < end;) {
+        const RowSpan row = row_span(c, cur.r, a.max_q);
+        const int u1 = (int)min((int64_t)cur.units, cur.u + (end - at));
+        const KeyRange tk = tile_keys(a, row, cur.r, R, cur.t);
+        const int unit0 = tk.lo / kUnitKeys;
+        int kb = a.whole ? tk.lo : max(tk.lo, (unit0 + cur.u) * kUnitKeys);
+        int ke = a.whole ? tk.hi : min(tk.hi, (unit0 + u1) * kUnitKeys);
+
+        // ---- this lane's query rows: qr + 8 i of each 16-row tile
+        int lo[2 * MT], hi[2 * MT], pos[2 * MT];
+        float fac[2 * MT], slope[2 * MT];
+        uint32_t qf[MT][KS][4];
+        int lo_min = 0x7fffffff, hi_max = 0, lo_max = 0, hi_min = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            const int ia = cur.t * R + qr + 8 * i;
+            const bool valid = ia < row.n * a.G;
+            const int tok = valid ? ia / a.G : 0, h = cur.g * a.G + (valid ? ia % a.G : 0);
+            KeyRange k = query_keys(a, row, cur.r, tok);
+            if (!valid) k = KeyRange{0, 0};
+            lo[i] = k.lo;
+            hi[i] = k.hi;
+            pos[i] = row.len - row.n + tok;
+            slope[i] = a.slopes ? a.slopes[h] * kLog2e : 0.f;
+            if (valid) {
+                if (k.lo < k.hi) {
+                    lo_min = min(lo_min, k.lo);
+                    hi_max = max(hi_max, k.hi);
+                }
+                lo_max = max(lo_max, k.lo);
+                hi_min = min(hi_min, k.hi);
+            }
+            // the row's elements d = (qc + 4 j) * 16 .. + 15
+            float f[D / 4];
+            float top = 0.f;
+            const __nv_bfloat16 *src = a.q + (int64_t)(row.t0 + tok) * a.q_stride + (int64_t)h * D;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 x = valid ? *reinterpret_cast<const uint4 *>(src + (qc + 4 * j) * 16 + 8 * e)
+                                          : make_uint4(0, 0, 0, 0);
+                    unpack8(x, f + 16 * j + 8 * e);
+                }
+#pragma unroll
+            for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(f[e]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            int ex = (int)(__float_as_uint(top) >> 23) - 127;
+            ex = top > 0.f && top < INFINITY ? min(max(ex, -126), 126) : 0;
+            const float down = __int_as_float((127 - ex) << 23), up = __int_as_float((127 + ex) << 23);
+            fac[i] = a.scale * up;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                qf[i / 2][s][i & 1] = pack_f16(f[4 * s] * down, f[4 * s + 1] * down);
+                qf[i / 2][s][2 + (i & 1)] = pack_f16(f[4 * s + 2] * down, f[4 * s + 3] * down);
+            }
+        }
+        if constexpr (MT > 1) {   // the fragments of two tiles do not fit the registers
+            if (warp == 0)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+                        *reinterpret_cast<uint4 *>(&sm.qf[((mt * KS + s) * 32 + lane) * 4]) =
+                            make_uint4(qf[mt][s][0], qf[mt][s][1], qf[mt][s][2], qf[mt][s][3]);
+            __syncthreads();
+        }
+        lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+        hi_max = __reduce_max_sync(0xffffffffu, hi_max);
+        lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+        hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+        kb = max(kb, lo_min);
+        ke = min(ke, hi_max);
+
+        const int kb0 = kb & ~(kTileKeys - 1);
+        const int tiles = ke > kb ? (ke - kb0 + kTileKeys - 1) / kTileKeys : 0;
+        const int mine = (tiles - warp + kWarps - 1) / kWarps;   // of this warp (tiles >= 0, warp < kWarps)
+        const int32_t *line = c.table + (int64_t)cur.r * c.max_pages;
+
+        // pages of the two halves of the warp's i-th tile (-2: no keys there, -1: no such page)
+        auto ids_of = [&](int i, int *id) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = kb0 + (warp + kWarps * i) * kTileKeys + 16 * h;
+                id[h] = -2;
+                if (i < mine && key < ke) {
+                    id[h] = line[key >> c.page_shift];
+                    if (id[h] < 0 || id[h] >= c.n_pages) {
+                        if (lane == 0) set_status(c.status, XGR_DEV_INDEX);
+                        id[h] = -1;
+                    }
+                }
+            }
+        };
+        auto issue = [&](int i, const int *id) {
+            if (i < mine) {
+                const int st = i % kStages;
+                const int key0 = kb0 + (warp + kWarps * i) * kTileKeys;
+                const uint32_t dst = ring0 + st * Smem<D, MT>::kStageBytes;
+#pragma unroll
+                for (int n = 0; n < kChunks; ++n) {          // 32 keys x kChunks chunks over 32 lanes
+                    const int idx = n * 32 + lane;
+                    const int kl = idx / kChunks, ch = idx % kChunks;
+                    const int page = kl < 16 ? id[0] : id[1];
+                    const bool in = page >= 0 && key0 + kl < ke;
+                    const int64_t off = in ? (((int64_t)page * c.Hkv + cur.g) * c.page + ((key0 + kl) & (c.page - 1))) * D + ch * 16
+                                           : 0;
+                    const uint32_t to = dst + kl * D + ((ch ^ swz<D>(kl)) << 4);
+                    cp_async16_zfill(to, c.k + off, in);
+                    cp_async16_zfill(to + kTileKeys * D, c.v + off, in);
+                }
+                if (lane < 4) {
+                    const int page = lane & 1 ? id[1] : id[0];
+                    const int64_t off = page >= 0 ? (int64_t)page * c.Hkv + cur.g : 0;
+                    cp_async4_zfill(sc0 + (st * 4 + lane) * 4, (lane < 2 ? c.ks : c.vs) + off, page >= 0);
+                }
+                if (lane == 0) sm.bad[warp][st] = (id[0] == -1 ? 1 : 0) | (id[1] == -1 ? 2 : 0);
+            }
+            cp_async_commit();
+        };
+
+        float o[MT][NT][4];
+        float m[2 * MT], l[2 * MT];
+        float vref = 1.17549435e-38f;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+
+        int id[2];
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            ids_of(i, id);
+            issue(i, id);
+        }
+        ids_of(kStages - 1, id);
+
+        for (int i = 0; i < mine; ++i) {
+            __syncwarp();                       // the slot about to be filled is read out
+            issue(i + kStages - 1, id);
+            ids_of(i + kStages, id);
+            cp_async_wait_group<kStages - 1>();
+            __syncwarp();
+            const int st = i % kStages;
+            const int key0 = kb0 + (warp + kWarps * i) * kTileKeys;
+            const uint8_t *kt = sm.ring[warp][st];
+            const uint8_t *vt = kt + kTileKeys * D;
+            const float4 sc = *reinterpret_cast<const float4 *>(sm.sc[warp][st]);
+            const int bad = sm.bad[warp][st];
+
+            // ---- S = Q K^T on the codes
+            float s[MT][4][4];
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                const int kl = nt * 8 + perm<D>(qr);
+                uint32_t kw[D / 16];
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(kt + kl * D + (((qc + 4 * j) ^ swz<D>(kl)) << 4));
+                    kw[4 * j] = x.x;
+                    kw[4 * j + 1] = x.y;
+                    kw[4 * j + 2] = x.z;
+                    kw[4 * j + 3] = x.w;
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    uint32_t b0, b1;
+                    codes_to_f16<FMT>(kw[ks], b0, b1);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        if constexpr (MT > 1) {
+                            const uint4 q = *reinterpret_cast<const uint4 *>(&sm.qf[((mt * KS + ks) * 32 + lane) * 4]);
+                            const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
+                            mma16816(s[mt][nt], qa, b0, b1);
+                        } else {
+                            mma16816(s[mt][nt], qf[mt][ks], b0, b1);
+                        }
+                    }
+                }
+            }
+
+            // ---- scores in log2 units, masked
+            const bool masked = key0 < lo_max || key0 + kTileKeys > hi_min || bad;
+            const float ksc[2] = {clean_scale(sc.x), clean_scale(sc.y)};
+            const float vsc[2] = {clean_scale(sc.z), clean_scale(sc.w)};
+#pragma unroll
+            for (int r2 = 0; r2 < 2 * MT; ++r2) {
+                const int mt = r2 / 2, e0 = 2 * (r2 & 1);
+                if (a.softcap > 0.f) {
+                    const float up = a.softcap * kLog2e;
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) {
+                        const float y = fac[r2] * ksc[nt / 2] * (2.f * kLog2e / a.softcap);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) s[mt][nt][e0 + e] = up * tanh_score(s[mt][nt][e0 + e] * y);
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) {
+                        const float y = fac[r2] * ksc[nt / 2] * kLog2e;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) s[mt][nt][e0 + e] *= y;
+                    }
+                }
+                if (a.slopes) {
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = key0 + nt * 8 + perm<D>(2 * qc + e);
+                            s[mt][nt][e0 + e] -= slope[r2] * fabsf((float)(pos[r2] - key));
+                        }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = key0 + nt * 8 + perm<D>(2 * qc + e);
+                            if (key < lo[r2] || key >= hi[r2] || (bad >> (nt / 2) & 1)) s[mt][nt][e0 + e] = -INFINITY;
+                        }
+                }
+            }
+
+            // ---- running maximum, weights
+            const float vnew = fmaxf(vref, fmaxf(vsc[0], vsc[1]));   // (fmaxf passes over a NaN)
+            const float vdown = vref / vnew;
+            const float vrel[2] = {vsc[0] / vnew, vsc[1] / vnew};
+            float alpha[2 * MT];
+            bool grew = vnew != vref;
+            vref = vnew;
+#pragma unroll
+            for (int r2 = 0; r2 < 2 * MT; ++r2) {
+                const int mt = r2 / 2, e0 = 2 * (r2 & 1);
+                float mx = -INFINITY;
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(s[mt][nt][e0], s[mt][nt][e0 + 1]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float m_new = fmaxf(m[r2], mx);
+                const float ref = m_new == -INFINITY ? 0.f : m_new;
+                alpha[r2] = exp2_fast(m[r2] - ref);      // 0 while nothing was seen
+                grew |= m_new != m[r2];
+                m[r2] = m_new;
+                const float bias = ref - kBias;
+                float sum = 0.f;
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = s[mt][nt][e0 + e];
+                        const float p = exp2_fast(x - bias);
+                        sum += p;
+                        // a key that is not seen weighs 0 even in a page whose scale is NaN
+                        s[mt][nt][e0 + e] = x == -INFINITY ? 0.f : p * vrel[nt / 2];
+                    }
+                l[r2] = l[r2] * alpha[r2] + sum;
+            }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int r2 = 0; r2 < 2 * MT; ++r2) {
+                    const float f = alpha[r2] * vdown;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        o[r2 / 2][n][2 * (r2 & 1)] *= f;
+                        o[r2 / 2][n][2 * (r2 & 1) + 1] *= f;
+                    }
+                }
+            }
+
+            // ---- O += W V on the codes
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t pa[MT][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    pa[mt][0] = pack_f16(s[mt][2 * u][0], s[mt][2 * u][1]);
+                    pa[mt][1] = pack_f16(s[mt][2 * u][2], s[mt][2 * u][3]);
+                    pa[mt][2] = pack_f16(s[mt][2 * u + 1][0], s[mt][2 * u + 1][1]);
+                    pa[mt][3] = pack_f16(s[mt][2 * u + 1][2], s[mt][2 * u + 1][3]);
+                }
+                uint32_t vw[4][D / 32];   // the lane's dims of its four keys
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int kl = 16 * u + (k / 2) * 8 + perm<D>(2 * qc + (k & 1));
+                    if constexpr (D == 128) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(vt + kl * D + ((perm<D>(qr) ^ swz<D>(kl)) << 4));
+                        vw[k][0] = x.x;
+                        vw[k][1] = x.y;
+                        vw[k][2] = x.z;
+                        vw[k][3] = x.w;
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(vt + kl * D + (((qr >> 1) ^ swz<D>(kl)) << 4) + (qr & 1) * 8);
+                        vw[k][0] = x.x;
+                        vw[k][1] = x.y;
+                    }
+                }
+#pragma unroll
+                for (int wd = 0; wd < D / 32; ++wd) {
+                    uint32_t b0[4], b1[4];
+                    codes_to_f16<FMT>(__byte_perm(vw[0][wd], vw[1][wd], 0x5140), b0[0], b0[1]);
+                    codes_to_f16<FMT>(__byte_perm(vw[0][wd], vw[1][wd], 0x7362), b0[2], b0[3]);
+                    codes_to_f16<FMT>(__byte_perm(vw[2][wd], vw[3][wd], 0x5140), b1[0], b1[1]);
+                    codes_to_f16<FMT>(__byte_perm(vw[2][wd], vw[3][wd], 0x7362), b1[2], b1[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * wd + e], pa[mt], b0[e], b1[e]);
+                }
+            }
+        }
+
+        // ---- join the warps
+        cp_async_wait_all();
+        __syncthreads();
+        float *ob = reinterpret_cast<float *>(smem_raw) + warp * R * D;   // over the rings
+#pragma unroll
+        for (int r2 = 0; r2 < 2 * MT; ++r2) {
+            float t = l[r2];
+            t += __shfl_xor_sync(0xffffffffu, t, 1);
+            t += __shfl_xor_sync(0xffffffffu, t, 2);
+            const int rr = qr + 8 * r2;
+            if (qc == 0) {
+                sm.m[warp][rr] = m[r2];
+                sm.l[warp][rr] = t;
+            }
+            // lane (qr, qc) holds, for each n tile, dims of n index 2 qc and 2 qc + 1
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int d0 = D == 128 ? perm<D>(2 * qc + e) * 16 : (2 * qc + e) * 8;
+#pragma unroll
+                for (int n = 0; n < NT; n += 4)
+                    *reinterpret_cast<float4 *>(ob + rr * D + d0 + n) =
+                        make_float4(o[r2 / 2][n][2 * (r2 & 1) + e], o[r2 / 2][n + 1][2 * (r2 & 1) + e],
+                                    o[r2 / 2][n + 2][2 * (r2 & 1) + e], o[r2 / 2][n + 3][2 * (r2 & 1) + e]);
+            }
+        }
+        if (lane == 0) sm.vref[warp] = vref;
+        __syncthreads();
+        const bool all = cur.u == 0 && u1 == cur.units;   // the whole segment was this block's
+        const int slot = cur.u == 0 ? 1 : 0;
+        const float *obase = reinterpret_cast<const float *>(smem_raw);
+        for (int idx = tid; idx < R * D / 8; idx += kThreads) {
+            const int rr = idx / (D / 8), d = (idx % (D / 8)) * 8;
+            const int ia = cur.t * R + rr;
+            if (ia >= row.n * a.G) continue;
+            float mm = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, sm.m[k][rr]);
+            const float ref = mm == -INFINITY ? 0.f : mm;
+            float lsum = 0.f, x[8] = {};
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float f = exp2_fast(sm.m[k][rr] - ref);
+                lsum += sm.l[k][rr] * f;
+                const float fv = f * sm.vref[k];
+                const float4 y0 = *reinterpret_cast<const float4 *>(obase + (k * R + rr) * D + d);
+                const float4 y1 = *reinterpret_cast<const float4 *>(obase + (k * R + rr) * D + d + 4);
+                x[0] += y0.x * fv; x[1] += y0.y * fv; x[2] += y0.z * fv; x[3] += y0.w * fv;
+                x[4] += y1.x * fv; x[5] += y1.y * fv; x[6] += y1.z * fv; x[7] += y1.w * fv;
+            }
+            if (all) {
+                const int64_t oi = (int64_t)(row.t0 + ia / a.G) * a.Hq + cur.g * a.G + ia % a.G;
+                const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+                uint4 pk;
+                __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&pk);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(x[2 * e] * inv, x[2 * e + 1] * inv);
+                *reinterpret_cast<uint4 *>(a.out + oi * D + d) = pk;
+                if (d == 0) a.lse[oi] = lsum == 0.f ? -INFINITY : (ref - kBias + log2f(lsum)) * kLn2;
+            } else {
+                const int64_t pi = ((int64_t)blockIdx.x * 2 + slot) * R + rr;
+                float4 *dst = reinterpret_cast<float4 *>(po.o + pi * D + d);
+                dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+                dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+                if (d == 0) po.ml[pi] = make_float2(mm, lsum);
+            }
+        }
+        __syncthreads();   // the rings and (m, l) are free for the next segment
+        at += u1 - cur.u;
+        if (at < end) plan_next(a, w, cur);
+        if (cur.r >= c.n_rows) break;
+    }
+}
+
+// A block per (token, query head): folds the partial results of a segment that
+// was cut.  O and l of part k count 2^(m_k - max m).
+template <int D>
+__global__ void __launch_bounds__(128) cache_join_kernel(AttendArgs a, RowsOf w, PlanOut po, int max_parts) {
+    extern __shared__ float wt[];   // [max_parts] weights
+    __shared__ float red[4];
+    __shared__ float acc[2][D];
+    griddep_wait();
+    griddep_launch_dependents();
+    const CacheArgs &c = a.c;
+    const int tok = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
+    int lo = 0, hi = c.n_rows - 1;
+    while (lo < hi) {   // the last row that begins at tok or before it
+        const int mid = (lo + hi + 1) / 2;
+        if (c.cu[mid] <= tok) lo = mid;
+        else hi = mid - 1;
+    }
+    const int r = lo;
+    const RowSpan row = row_span(c, r, a.max_q);
+    if (tok < row.t0 || tok >= row.t0 + row.n || !w.mine((int64_t)row.n * a.G)) return;
+    const int g = h / a.G, ia = (tok - row.t0) * a.G + h % a.G;
+    const int t = ia / w.R, rr = ia % w.R;
+    int64_t u = po.row_unit[r];
+    for (int i = 0; i < t; ++i) u += (int64_t)range_units(a, tile_keys(a, row, r, w.R, i)) * c.Hkv;
+    const int units = range_units(a, tile_keys(a, row, r, w.R, t));
+    u += (int64_t)g * units;
+    const int64_t per = *po.per;
+    const int c0 = (int)(u / per), c1 = (int)((u + units - 1) / per);
+    const int n = c1 - c0 + 1;
+    if (n == 1 || n > max_parts) return;   // (written whole)
+    auto part = [&](int k) { return ((int64_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * w.R + rr; };
+    const int tid = threadIdx.x, lane = tid % 32;
+    float m = -INFINITY;
+    for (int k = tid; k < n; k += 128) m = fmaxf(m, po.ml[part(k)].x);
+    m = warp_max(m);
+    if (lane == 0) red[tid / 32] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    __syncthreads();
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (int k = tid; k < n; k += 128) {
+        const float2 ml = po.ml[part(k)];
+        const float f = exp2_fast(ml.x - ref);
+        wt[k] = f;
+        l += f * ml.y;
+    }
+    l = warp_sum(l);
+    if (lane == 0) red[tid / 32] = l;
+    __syncthreads();
+    l = red[0] + red[1] + red[2] + red[3];
+    const int d = tid % D, half = tid / D;           // D = 64: two threads a dim
+    constexpr int kSplit = 128 / D;
+    float x = 0.f;
+#pragma unroll 8
+    for (int k = half; k < n; k += kSplit) x += wt[k] * po.o[part(k) * D + d];
+    if constexpr (kSplit == 2) {
+        acc[half][d] = x;
+        __syncthreads();
+        x = acc[0][d] + acc[1][d];
+    }
+    if (half == 0) {
+        const int64_t oi = (int64_t)tok * a.Hq + h;
+        a.out[oi * D + d] = __float2bfloat16(l == 0.f ? 0.f : x / l);
+        if (d == 0) a.lse[oi] = l == 0.f ? -INFINITY : (ref - kBias + log2f(l)) * kLn2;
+    }
+}
+
+constexpr int kSmallCtas = 3 * kSms;         // 16-row tiles: three CTAs an SM
+constexpr int kWideCtas = 2 * kSms;          // 32-row tiles: two
+constexpr int kMinUnits = 4;                 // fewest units a CTA takes (512 keys): below, joining costs more than it spreads
+constexpr int kWholeUnits = 8;               // rows of at most this many units are not cut
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct WsLayout {
+    size_t rows, per, o, ml, total;
+};
+WsLayout ws_layout(int D, int n_rows) {
+    WsLayout w{};
+    w.rows = 0;
+    w.per = up256((size_t)n_rows * 8);
+    w.o = w.per + 256;
+    const size_t parts = 2 * std::max<size_t>(kSmallCtas * 16, kWideCtas * 32);
+    w.ml = w.o + up256(parts * D * 4);
+    w.total = w.ml + up256(parts * 8);
+    return w;
+}
+
+template <int D, int FMT, int MT>
+cudaError_t launch_mt(const AttendArgs &a, cudaStream_t s) {
+    const size_t smem = sizeof(Smem<D, MT>);
+    static bool ready[kMaxDevices] = {};   // the attribute is set on the first (uncaptured) launch of a device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(cache_attend_kernel<D, FMT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        ready[dev] = true;
+    }
+    const WsLayout l = ws_layout(D, a.c.n_rows);
+    PlanOut po{};
+    if (!a.whole) {
+        po.row_unit = reinterpret_cast<int64_t *>(a.ws + l.rows);
+        po.per = reinterpret_cast<int64_t *>(a.ws + l.per);
+        po.o = reinterpret_cast<float *>(a.ws + l.o);
+        po.ml = reinterpret_cast<float2 *>(a.ws + l.ml);
+    }
+    constexpr int R = 16 * MT;
+    const RowsOf w{0, 0x7fffffff, R};
+    // no more CTAs than there can be units
+    const int64_t row_pages = (int64_t)a.c.max_pages * a.c.page / kUnitKeys + 2;
+    const int64_t segs = (((int64_t)a.c.n_tokens * a.G + R - 1) / R + a.c.n_rows) * a.c.Hkv;
+    const int64_t units = a.whole ? segs : (segs * row_pages + kMinUnits - 1) / kMinUnits;
+    const int ctas = (int)std::min<int64_t>(MT == 1 ? kSmallCtas : kWideCtas, units);
+    e = launch_pdl(cache_attend_kernel<D, FMT, MT>, dim3(ctas), dim3(kThreads), smem, s, a, w, po,
+                   a.whole ? 1 : kMinUnits);
+    if (e != cudaSuccess || a.whole) return e;
+    return launch_pdl(cache_join_kernel<D>, dim3((unsigned)((int64_t)a.c.n_tokens * a.Hq)), dim3(128),
+                      (size_t)ctas * 4, s, a, w, po, ctas);
+}
+
+template <int D, int FMT>
+cudaError_t launch_fmt(const AttendArgs &a, cudaStream_t s) {
+    if ((int64_t)a.max_q * a.G <= 16) return launch_mt<D, FMT, 1>(a, s);
+    return launch_mt<D, FMT, 2>(a, s);
+}
+
+}  // namespace
+
+size_t attend_ws_bytes(int D, int n_rows) { return ws_layout(D, n_rows).total; }
+
+cudaError_t launch_cache_attend(const AttendArgs &in, cudaStream_t s) {
+    AttendArgs a = in;
+    a.whole = (int64_t)a.c.max_pages * a.c.page <= kWholeUnits * kUnitKeys;
+    if (a.c.D == 128)
+        return a.c.fmt == XGR_CACHE_E4M3 ? launch_fmt<128, XGR_CACHE_E4M3>(a, s) : launch_fmt<128, XGR_CACHE_INT8>(a, s);
+    return a.c.fmt == XGR_CACHE_E4M3 ? launch_fmt<64, XGR_CACHE_E4M3>(a, s) : launch_fmt<64, XGR_CACHE_INT8>(a, s);
+}
+
+}  // namespace xgr

@@ -1,0 +1,196 @@
+// cache_plan.cuh -- how the attention over the paged cache is cut into work
+// (internal; shared by its kernels).
+//
+// A row's query rows (new tokens x query heads of a kv head, token-major) are
+// cut into tiles of R; a segment is (row, tile, kv head) and its keys are cut
+// into units of kUnitKeys.  All units of all segments form one line, and CTA c
+// of N takes units [c * per, (c + 1) * per): rows of any raggedness load the
+// CTAs evenly, however few they are.  A segment cut by a CTA's end leaves
+// partial results (O relative to its reference, m, l) in the workspace, at most
+// two a CTA (the segment it continues, slot 0, and the one it leaves
+// unfinished, slot 1), and the join kernel folds them.  Lengths are read on the
+// device, so nothing waits for the host; every CTA works the plan out anew
+// from d_cu and d_len, and the first one leaves it for the join.
+//
+// In "whole" mode (every row is short) a unit is a whole segment: nothing is
+// cut and no join runs.
+#pragma once
+
+#include "cache.cuh"
+
+namespace xgr {
+
+constexpr int kUnitKeys = 128;
+
+// Results of a segment or of a part of it are joined from these.
+struct PlanOut {
+    int64_t *row_unit;   // [n_rows] first unit of each row
+    int64_t *per;        // [1] units a CTA takes
+    float *o;            // [N][2][R][D]
+    float2 *ml;          // [N][2][R]
+};
+
+// The keys [lo, hi) that some query of tile t may see, by position alone
+// (d_first can only narrow it), of a row with span s.
+struct KeyRange {
+    int lo, hi;
+};
+
+__device__ __forceinline__ KeyRange tile_keys(const AttendArgs &a, const RowSpan &s, int r, int R, int t) {
+    KeyRange k{0, s.len};
+    const int i0 = t * R / a.G, i1 = (min((t + 1) * R, s.n * a.G) - 1) / a.G;   // its tokens
+    const int p0 = s.len - s.n;
+    if (a.causal) {
+        k.hi = p0 + i1 + 1;
+        if (a.prefix) k.hi = max(k.hi, min(a.prefix[r], s.len));
+    }
+    if (a.window > 0) k.lo = max(0, p0 + i0 - a.window + 1);
+    return k;
+}
+
+__device__ __forceinline__ int range_units(const AttendArgs &a, const KeyRange &k) {
+    if (a.whole) return 1;
+    return max(1, (k.hi + kUnitKeys - 1) / kUnitKeys - k.lo / kUnitKeys);
+}
+
+// Rows whose query rows lie in (min_rows, max_rows] are this kernel's.
+struct RowsOf {
+    int min_rows, max_rows, R;
+    __device__ bool mine(int64_t rows) const { return rows > min_rows && rows <= max_rows; }
+};
+
+__device__ __forceinline__ int64_t row_units(const AttendArgs &a, const RowSpan &s, int r, const RowsOf &w) {
+    const int64_t rows = (int64_t)s.n * a.G;
+    if (s.n == 0 || !w.mine(rows)) return 0;
+    const int tiles = (int)((rows + w.R - 1) / w.R);
+    int64_t u = 0;
+    for (int t = 0; t < tiles; ++t) u += range_units(a, tile_keys(a, s, r, w.R, t));
+    return u * a.c.Hkv;
+}
+
+// Where a CTA stands in the line.
+struct Cursor {
+    int r, t, g;     // segment
+    int u;           // unit within it
+    int units;       // its units
+};
+
+// Every thread of the block gets the block's first cursor and [begin, end)
+// (false: no work).  T = threads of the block.
+template <int T>
+__device__ __forceinline__ bool plan_begin(const AttendArgs &a, const RowsOf &w, int min_units,
+                                           const PlanOut &p, Cursor &cur, int64_t &begin, int64_t &end,
+                                           int64_t &per) {
+    __shared__ int64_t base[T / 32 + 1];
+    __shared__ Cursor first;
+    const int n_rows = a.c.n_rows;
+    const int rpt = (n_rows + T - 1) / T;
+    const int r0 = min((int)threadIdx.x * rpt, n_rows), r1 = min(r0 + rpt, n_rows);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) mine += row_units(a, row_span(a.c, r, a.max_q), r, w);
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) base[warp + 1] = x;
+    if (threadIdx.x == 0) base[0] = 0;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int i = 0; i < T / 32; ++i) base[i + 1] += base[i];
+    __syncthreads();
+    const int64_t total = base[T / 32];
+    const int64_t from = base[warp] + x - mine;   // first unit of this thread's rows
+    per = max((int64_t)min_units, (total + gridDim.x - 1) / gridDim.x);
+    begin = blockIdx.x * per;
+    end = min(begin + per, total);
+    if (blockIdx.x == 0 && p.row_unit) {
+        int64_t at = from;
+        for (int r = r0; r < r1; ++r) {
+            p.row_unit[r] = at;
+            at += row_units(a, row_span(a.c, r, a.max_q), r, w);
+        }
+        if (threadIdx.x == 0) *p.per = per;
+    }
+    if (begin >= end) return false;
+    if (from <= begin && begin < from + mine) {
+        int64_t left = begin - from;
+        int r = r0;
+        for (; r < r1 - 1; ++r) {
+            const int64_t u = row_units(a, row_span(a.c, r, a.max_q), r, w);
+            if (left < u) break;
+            left -= u;
+        }
+        const RowSpan s = row_span(a.c, r, a.max_q);
+        const int tiles = (int)(((int64_t)s.n * a.G + w.R - 1) / w.R);
+        int t = 0, units = 1;
+        for (; t < tiles; ++t) {
+            units = range_units(a, tile_keys(a, s, r, w.R, t));
+            if (left < (int64_t)units * a.c.Hkv) break;
+            left -= (int64_t)units * a.c.Hkv;
+        }
+        first.r = r;
+        first.t = t;
+        first.g = (int)(left / units);
+        first.u = (int)(left % units);
+        first.units = units;
+    }
+    __syncthreads();
+    cur = first;
+    return true;
+}
+
+// The segment after cur; cur.r = n_rows behind the last one.
+__device__ __forceinline__ void plan_next(const AttendArgs &a, const RowsOf &w, Cursor &cur) {
+    cur.u = 0;
+    if (++cur.g < a.c.Hkv) return;
+    cur.g = 0;
+    ++cur.t;
+    for (; cur.r < a.c.n_rows; ++cur.r, cur.t = 0) {
+        const RowSpan s = row_span(a.c, cur.r, a.max_q);
+        const int64_t rows = (int64_t)s.n * a.G;
+        if (s.n == 0 || !w.mine(rows) || (int64_t)cur.t * w.R >= rows) continue;
+        cur.units = range_units(a, tile_keys(a, s, cur.r, w.R, cur.t));
+        return;
+    }
+}
+
+// Query i of row span s at position pos sees [lo, hi).
+__device__ __forceinline__ KeyRange query_keys(const AttendArgs &a, const RowSpan &s, int r, int i) {
+    const int pos = s.len - s.n + i;
+    KeyRange k{0, s.len};
+    if (a.causal) {
+        k.hi = pos + 1;
+        if (a.prefix) k.hi = max(k.hi, min(a.prefix[r], s.len));
+    }
+    if (a.window > 0) k.lo = max(0, pos - a.window + 1);
+    if (a.first) k.lo = max(k.lo, a.first[s.t0 + i]);
+    return k;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {   // one MUFU op; tiny results flush to 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// c * tanh(y) with tanh from one exponential and one reciprocal: 1 - 2 / (1 + e^2y).
+// Its error is a few 2^-24 absolute, which is what counts in an exponent; the
+// hardware's own tanh (about 2^-11) would put 2 % on a weight at a cap of 50.
+__device__ __forceinline__ float tanh_score(float y2) {   // y2 = 2 log2(e) y
+    return 1.f - __fdividef(2.f, 1.f + exp2_fast(y2));
+}
+
+// V scales and K scales: finite and non-negative, or NaN for a page that got a
+// NaN or an infinity; an infinite one counts as NaN.
+__device__ __forceinline__ float clean_scale(float s) {
+    return fabsf(s) < INFINITY ? s : __int_as_float(0x7fc00000);
+}
+
+// The weights are kept as 2^14 p (fp16 in the products): p <= 1 leaves the top
+// of fp16's range, so a weight as small as 2^-38 of the row's largest still counts.
+constexpr float kBias = 14.f;
+
+}  // namespace xgr

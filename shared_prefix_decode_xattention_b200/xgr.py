@@ -43,6 +43,10 @@ XGR_MASK_DENSE = 0
 XGR_MASK_CSR = 1
 XGR_MASK_NODE_BITS = 2
 XGR_MASK_TRIE_ROWS = 3
+XGR_CACHE_E4M3 = 0
+XGR_CACHE_INT8 = 1
+XGR_ATTN_FULL = 0
+XGR_ATTN_CAUSAL = 1
 
 
 class XgrError(RuntimeError):
@@ -86,6 +90,41 @@ class xgr_mask(ctypes.Structure):
     ]
 
 
+class xgr_cache(ctypes.Structure):
+    _fields_ = [
+        ("d_k", ctypes.c_void_p),
+        ("d_v", ctypes.c_void_p),
+        ("d_k_scale", ctypes.c_void_p),
+        ("d_v_scale", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+    ]
+
+
+class xgr_cache_rows(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("d_table", ctypes.c_void_p),
+        ("d_len", ctypes.c_void_p),
+    ]
+
+
+class xgr_attn_opts(ctypes.Structure):
+    _fields_ = [
+        ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("mask", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("d_slopes", ctypes.c_void_p),
+        ("d_prefix", ctypes.c_void_p),
+        ("d_first", ctypes.c_void_p),
+    ]
+
+
 class xgr_decode_group(ctypes.Structure):
     _fields_ = [
         ("ctx", ctypes.c_void_p),
@@ -126,6 +165,7 @@ def lib():
                            "shared_prefix_decode_xattention_b200.build.build()")
     L = ctypes.CDLL(LIB_PATH)
     P, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    PC, PR, PZ = ctypes.POINTER(xgr_cache), ctypes.POINTER(xgr_cache_rows), ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "xgr_workspace_bytes": [ctypes.POINTER(xgr_config), ctypes.POINTER(ctypes.c_size_t)],
         "xgr_create": [ctypes.POINTER(xgr_config), P, ctypes.c_size_t, ctypes.POINTER(P)],
@@ -147,6 +187,15 @@ def lib():
         "xgr_decode_graph_launch": [P, P],
         "xgr_decode_graph_kernels": [P, ctypes.POINTER(i32)],
         "xgr_decode_graph_destroy": [P],
+        # the paged 8-bit KV cache (include/xgr_cache.h)
+        "xgr_cache_attend_bytes": [PC, i32, i32, PZ],
+        "xgr_cache_attend": [PC, PR, P, i32, i32, i32, P, i64, ctypes.POINTER(xgr_attn_opts), P, P, P,
+                             ctypes.c_size_t, P, P],
+        "xgr_cache_store": [PC, PR, P, i32, i32, P, P, i64, P, P],
+        "xgr_cache_fork_bytes": [PC, i32, PZ],
+        "xgr_cache_fork": [PC, PR, i32, P, P, P, P, P, ctypes.c_size_t, P, P],
+        "xgr_cache_compact_bytes": [PC, PZ],
+        "xgr_cache_compact": [PC, PR, P, P, P, ctypes.c_size_t, P, P],
         # host-side batch former (include/xgr_sched.h)
         "xgr_cht_create": [i32, ctypes.POINTER(P)],
         "xgr_cht_destroy": [P],
@@ -345,6 +394,57 @@ def xgr_decode_graph_kernels(graph: int) -> int:
 
 def xgr_decode_graph_destroy(graph: int) -> None:
     _check("xgr_decode_graph_destroy", lib().xgr_decode_graph_destroy(graph))
+
+
+# ---- the paged 8-bit KV cache (include/xgr_cache.h; cache.PagedCache wraps these)
+
+def xgr_cache_attend_bytes(cache: xgr_cache, n_q_heads: int, n_rows: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("xgr_cache_attend_bytes",
+           lib().xgr_cache_attend_bytes(ctypes.byref(cache), n_q_heads, n_rows, ctypes.byref(n)))
+    return n.value
+
+
+def xgr_cache_attend(cache: xgr_cache, rows: xgr_cache_rows, cu, n_tokens: int, max_q: int,
+                     n_q_heads: int, q, q_stride: int, opts: xgr_attn_opts, out, lse, ws, ws_bytes: int,
+                     status, stream=None) -> None:
+    _check("xgr_cache_attend", lib().xgr_cache_attend(
+        ctypes.byref(cache), ctypes.byref(rows), _ptr(cu), n_tokens, max_q, n_q_heads, _ptr(q), q_stride,
+        ctypes.byref(opts), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _ptr(status), _stream(stream)))
+
+
+def xgr_cache_store(cache: xgr_cache, rows: xgr_cache_rows, cu, n_tokens: int, max_n: int, k, v,
+                    token_stride: int, status, stream=None) -> None:
+    _check("xgr_cache_store", lib().xgr_cache_store(
+        ctypes.byref(cache), ctypes.byref(rows), _ptr(cu), n_tokens, max_n, _ptr(k), _ptr(v),
+        token_stride, _ptr(status), _stream(stream)))
+
+
+def xgr_cache_fork_bytes(cache: xgr_cache, n_out: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("xgr_cache_fork_bytes",
+           lib().xgr_cache_fork_bytes(ctypes.byref(cache), n_out, ctypes.byref(n)))
+    return n.value
+
+
+def xgr_cache_fork(cache: xgr_cache, rows: xgr_cache_rows, n_out: int, parent, n_new, table_out, len_out,
+                   ws, ws_bytes: int, status, stream=None) -> None:
+    _check("xgr_cache_fork", lib().xgr_cache_fork(
+        ctypes.byref(cache), ctypes.byref(rows), n_out, _ptr(parent), _ptr(n_new), _ptr(table_out),
+        _ptr(len_out), _ptr(ws), ws_bytes, _ptr(status), _stream(stream)))
+
+
+def xgr_cache_compact_bytes(cache: xgr_cache) -> int:
+    n = ctypes.c_size_t(0)
+    _check("xgr_cache_compact_bytes", lib().xgr_cache_compact_bytes(ctypes.byref(cache), ctypes.byref(n)))
+    return n.value
+
+
+def xgr_cache_compact(cache: xgr_cache, rows: xgr_cache_rows, table_out, n_used, ws, ws_bytes: int,
+                      status, stream=None) -> None:
+    _check("xgr_cache_compact", lib().xgr_cache_compact(
+        ctypes.byref(cache), ctypes.byref(rows), _ptr(table_out), _ptr(n_used), _ptr(ws), ws_bytes,
+        _ptr(status), _stream(stream)))
 
 
 def make_config(**kw) -> xgr_config:

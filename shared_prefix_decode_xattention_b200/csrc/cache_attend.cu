@@ -24,6 +24,7 @@
 // dims of four keys: conversion needs no shuffles, the weights' fragments are
 // the scores' own registers, and all shared-memory reads are 16 bytes wide and
 // free of bank conflicts (perm and swz below).
+#include "cache_codes.cuh"
 #include "cache_plan.cuh"
 
 namespace xgr {
@@ -75,32 +76,8 @@ __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// the four codes of a word -> two fp16 pairs (elements 0, 1 and 2, 3)
-template <int FMT>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    if constexpr (FMT == XGR_CACHE_E4M3) {
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-            : "=r"(lo), "=r"(hi)
-            : "r"(w));
-    } else {   // 1024 + (code + 128) is an fp16 number with the byte as its low bits
-        const uint32_t u = w ^ 0x80808080u;
-        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
-        const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&l), off);
-        const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&h), off);
-        lo = *reinterpret_cast<const uint32_t *>(&a);
-        hi = *reinterpret_cast<const uint32_t *>(&b);
-    }
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 template <int D, int FMT, int MT>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel(AttendArgs a, RowsOf w, PlanOut po,
+__global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel(AttendArgs a, PlanOut po,
                                                                               int min_units) {
     constexpr int R = 16 * MT;
     constexpr int KS = D / 16;                 // k steps of Q K^T
@@ -116,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
     griddep_launch_dependents();
     Cursor cur;
     int64_t begin, end, per;
-    if (!plan_begin<kThreads>(a, w, min_units, po, cur, begin, end, per)) return;
+    if (!plan_begin<kThreads>(a, R, min_units, po, cur, begin, end, per)) return;
 
     const uint32_t ring0 = smem_u32(&sm.ring[warp][0][0]);
     const uint32_t sc0 = smem_u32(&sm.sc[warp][0][0]);
@@ -169,10 +146,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
             for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(f[e]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            int ex = (int)(__float_as_uint(top) >> 23) - 127;
-            ex = top > 0.f && top < INFINITY ? min(max(ex, -126), 126) : 0;
-            const float down = __int_as_float((127 - ex) << 23), up = __int_as_float((127 + ex) << 23);
-            fac[i] = a.scale * up;
+            const int ex = query_exp(top);
+            const float down = pow2i(-ex);
+            fac[i] = a.scale * pow2i(ex);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 qf[i / 2][s][i & 1] = pack_f16(f[4 * s] * down, f[4 * s + 1] * down);
@@ -513,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
         }
         __syncthreads();   // the rings and (m, l) are free for the next segment
         at += u1 - cur.u;
-        if (at < end) plan_next(a, w, cur);
+        if (at < end) plan_next(a, R, cur);
         if (cur.r >= c.n_rows) break;
     }
 }
@@ -521,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
 // A block per (token, query head): folds the partial results of a segment that
 // was cut.  O and l of part k count 2^(m_k - max m).
 template <int D>
-__global__ void __launch_bounds__(128) cache_join_kernel(AttendArgs a, RowsOf w, PlanOut po, int max_parts) {
+__global__ void __launch_bounds__(128) cache_join_kernel(AttendArgs a, int R, PlanOut po, int max_parts, float bias) {
     extern __shared__ float wt[];   // [max_parts] weights
     __shared__ float red[4];
     __shared__ float acc[2][D];
@@ -537,18 +513,18 @@ __global__ void __launch_bounds__(128) cache_join_kernel(AttendArgs a, RowsOf w,
     }
     const int r = lo;
     const RowSpan row = row_span(c, r, a.max_q);
-    if (tok < row.t0 || tok >= row.t0 + row.n || !w.mine((int64_t)row.n * a.G)) return;
+    if (tok < row.t0 || tok >= row.t0 + row.n) return;
     const int g = h / a.G, ia = (tok - row.t0) * a.G + h % a.G;
-    const int t = ia / w.R, rr = ia % w.R;
+    const int t = ia / R, rr = ia % R;
     int64_t u = po.row_unit[r];
-    for (int i = 0; i < t; ++i) u += (int64_t)range_units(a, tile_keys(a, row, r, w.R, i)) * c.Hkv;
-    const int units = range_units(a, tile_keys(a, row, r, w.R, t));
+    for (int i = 0; i < t; ++i) u += (int64_t)range_units(a, tile_keys(a, row, r, R, i)) * c.Hkv;
+    const int units = range_units(a, tile_keys(a, row, r, R, t));
     u += (int64_t)g * units;
     const int64_t per = *po.per;
     const int c0 = (int)(u / per), c1 = (int)((u + units - 1) / per);
     const int n = c1 - c0 + 1;
     if (n == 1 || n > max_parts) return;   // (written whole)
-    auto part = [&](int k) { return ((int64_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * w.R + rr; };
+    auto part = [&](int k) { return ((int64_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * R + rr; };
     const int tid = threadIdx.x, lane = tid % 32;
     float m = -INFINITY;
     for (int k = tid; k < n; k += 128) m = fmaxf(m, po.ml[part(k)].x);
@@ -582,12 +558,13 @@ __global__ void __launch_bounds__(128) cache_join_kernel(AttendArgs a, RowsOf w,
     if (half == 0) {
         const int64_t oi = (int64_t)tok * a.Hq + h;
         a.out[oi * D + d] = __float2bfloat16(l == 0.f ? 0.f : x / l);
-        if (d == 0) a.lse[oi] = l == 0.f ? -INFINITY : (ref - kBias + log2f(l)) * kLn2;
+        if (d == 0) a.lse[oi] = l == 0.f ? -INFINITY : (ref - bias + log2f(l)) * kLn2;
     }
 }
 
 constexpr int kSmallCtas = 3 * kSms;         // 16-row tiles: three CTAs an SM
 constexpr int kWideCtas = 2 * kSms;          // 32-row tiles: two
+constexpr int kTcRows256 = 256;              // tcgen05 tiles: one
 constexpr int kMinUnits = 4;                 // fewest units a CTA takes (512 keys): below, joining costs more than it spreads
 constexpr int kWholeUnits = 8;               // rows of at most this many units are not cut
 
@@ -601,14 +578,14 @@ WsLayout ws_layout(int D, int n_rows) {
     w.rows = 0;
     w.per = up256((size_t)n_rows * 8);
     w.o = w.per + 256;
-    const size_t parts = 2 * std::max<size_t>(kSmallCtas * 16, kWideCtas * 32);
+    const size_t parts = 2 * std::max<size_t>({(size_t)kSmallCtas * 16, (size_t)kWideCtas * 32, (size_t)kSms * kTcRows256});
     w.ml = w.o + up256(parts * D * 4);
     w.total = w.ml + up256(parts * 8);
     return w;
 }
 
 template <int D, int FMT, int MT>
-cudaError_t launch_mt(const AttendArgs &a, cudaStream_t s) {
+cudaError_t launch_small(const AttendArgs &a, const PlanOut &po, int ctas, int min_units, cudaStream_t s) {
     const size_t smem = sizeof(Smem<D, MT>);
     static bool ready[kMaxDevices] = {};   // the attribute is set on the first (uncaptured) launch of a device
     int dev = 0;
@@ -620,32 +597,14 @@ cudaError_t launch_mt(const AttendArgs &a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    const WsLayout l = ws_layout(D, a.c.n_rows);
-    PlanOut po{};
-    if (!a.whole) {
-        po.row_unit = reinterpret_cast<int64_t *>(a.ws + l.rows);
-        po.per = reinterpret_cast<int64_t *>(a.ws + l.per);
-        po.o = reinterpret_cast<float *>(a.ws + l.o);
-        po.ml = reinterpret_cast<float2 *>(a.ws + l.ml);
-    }
-    constexpr int R = 16 * MT;
-    const RowsOf w{0, 0x7fffffff, R};
-    // no more CTAs than there can be units
-    const int64_t row_pages = (int64_t)a.c.max_pages * a.c.page / kUnitKeys + 2;
-    const int64_t segs = (((int64_t)a.c.n_tokens * a.G + R - 1) / R + a.c.n_rows) * a.c.Hkv;
-    const int64_t units = a.whole ? segs : (segs * row_pages + kMinUnits - 1) / kMinUnits;
-    const int ctas = (int)std::min<int64_t>(MT == 1 ? kSmallCtas : kWideCtas, units);
-    e = launch_pdl(cache_attend_kernel<D, FMT, MT>, dim3(ctas), dim3(kThreads), smem, s, a, w, po,
-                   a.whole ? 1 : kMinUnits);
-    if (e != cudaSuccess || a.whole) return e;
-    return launch_pdl(cache_join_kernel<D>, dim3((unsigned)((int64_t)a.c.n_tokens * a.Hq)), dim3(128),
-                      (size_t)ctas * 4, s, a, w, po, ctas);
+    return launch_pdl(cache_attend_kernel<D, FMT, MT>, dim3(ctas), dim3(kThreads), smem, s, a, po, min_units);
 }
 
 template <int D, int FMT>
-cudaError_t launch_fmt(const AttendArgs &a, cudaStream_t s) {
-    if ((int64_t)a.max_q * a.G <= 16) return launch_mt<D, FMT, 1>(a, s);
-    return launch_mt<D, FMT, 2>(a, s);
+cudaError_t launch_kind(const AttendArgs &a, int R, const PlanOut &po, int ctas, int min_units, cudaStream_t s) {
+    if (R == 16) return launch_small<D, FMT, 1>(a, po, ctas, min_units, s);
+    if (R == 32) return launch_small<D, FMT, 2>(a, po, ctas, min_units, s);
+    return launch_attend_tc(a, po, ctas, min_units, s);
 }
 
 }  // namespace
@@ -654,10 +613,37 @@ size_t attend_ws_bytes(int D, int n_rows) { return ws_layout(D, n_rows).total; }
 
 cudaError_t launch_cache_attend(const AttendArgs &in, cudaStream_t s) {
     AttendArgs a = in;
-    a.whole = (int64_t)a.c.max_pages * a.c.page <= kWholeUnits * kUnitKeys;
-    if (a.c.D == 128)
-        return a.c.fmt == XGR_CACHE_E4M3 ? launch_fmt<128, XGR_CACHE_E4M3>(a, s) : launch_fmt<128, XGR_CACHE_INT8>(a, s);
-    return a.c.fmt == XGR_CACHE_E4M3 ? launch_fmt<64, XGR_CACHE_E4M3>(a, s) : launch_fmt<64, XGR_CACHE_INT8>(a, s);
+    const CacheArgs &c = a.c;
+    a.whole = (int64_t)c.max_pages * c.page <= kWholeUnits * kUnitKeys;
+    // 16 or 32 query rows a tile on mma.sync while no row has more; else 256 a tile on tcgen05
+    const int64_t most = (int64_t)a.max_q * a.G;
+    const int R = most <= 16 ? 16 : most <= 32 ? 32 : kTcRows256;
+    const int cap = R == 16 ? kSmallCtas : R == 32 ? kWideCtas : kSms;
+    const int min_units = a.whole ? 1 : kMinUnits;
+    // no more CTAs than there can be shares of the line
+    const int64_t segs = (((int64_t)c.n_tokens * a.G + R - 1) / R + c.n_rows) * c.Hkv;
+    const int64_t row_units = a.whole ? 1 : (int64_t)c.max_pages * c.page / kUnitKeys + 2;
+    const int ctas = (int)std::min<int64_t>(cap, (segs * row_units + min_units - 1) / min_units);
+    PlanOut po{};
+    if (!a.whole) {
+        const WsLayout l = ws_layout(c.D, c.n_rows);
+        po.row_unit = reinterpret_cast<int64_t *>(a.ws + l.rows);
+        po.per = reinterpret_cast<int64_t *>(a.ws + l.per);
+        po.o = reinterpret_cast<float *>(a.ws + l.o);
+        po.ml = reinterpret_cast<float2 *>(a.ws + l.ml);
+    }
+    cudaError_t e;
+    if (c.D == 128)
+        e = c.fmt == XGR_CACHE_E4M3 ? launch_kind<128, XGR_CACHE_E4M3>(a, R, po, ctas, min_units, s)
+                                    : launch_kind<128, XGR_CACHE_INT8>(a, R, po, ctas, min_units, s);
+    else
+        e = c.fmt == XGR_CACHE_E4M3 ? launch_kind<64, XGR_CACHE_E4M3>(a, R, po, ctas, min_units, s)
+                                    : launch_kind<64, XGR_CACHE_INT8>(a, R, po, ctas, min_units, s);
+    if (e != cudaSuccess || a.whole) return e;
+    const dim3 grid((unsigned)((int64_t)c.n_tokens * a.Hq));
+    const float bias = R == kTcRows256 ? kTcBias : kBias;
+    return c.D == 128 ? launch_pdl(cache_join_kernel<128>, grid, dim3(128), (size_t)ctas * 4, s, a, R, po, ctas, bias)
+                      : launch_pdl(cache_join_kernel<64>, grid, dim3(128), (size_t)ctas * 4, s, a, R, po, ctas, bias);
 }
 
 }  // namespace xgr

@@ -1,0 +1,615 @@
+// cache_attend_tc.cu -- attention over the paged 8-bit cache for rows with
+// many query rows (a chunk of a prompt, the beams of a request over its shared
+// prompt), on the 5th-generation tensor cores.
+//
+// The mathematics is that of cache_attend.cu: the products take the codes
+// themselves as fp16 numbers, the scales stay outside.  Here the exponent of
+// the V scale joins the score: t_j = x_j log2 e + log2 b_j is the exponent of
+// the weight w_j = b_j p_j, one lazily raised reference M per row bounds it
+// (raised when a chunk passes it by more than 2^8), and l sums w_j / b_j, so
+// neither scale costs an instruction per score.  Rounded are the weights (fp16)
+// and the output (bf16); all else is fp32.
+//
+// One CTA per SM, persistent over its share of the work line (cache_plan.cuh);
+// a tile is 256 query rows, two products of 128 rows; 16 warps:
+//   warps 0-7    two softmax warpgroups, a query row a thread: scores from
+//                tensor memory, cap, bias, mask, weights back over the scores'
+//                buffer as fp16, and at a segment's end the output;
+//   warps 8-11   the codes of each 128-key chunk, 16 bytes a load straight from
+//                the pages into registers one chunk ahead, converted and written
+//                as the 128-byte-swizzled operands of K and V (rings of two);
+//   warp 12      issues the products: S_h = Q_h K^T, O_h += W_h V, whichever of
+//                the two tiles is ready, so one tile's softmax runs beside the
+//                other's products.
+// A conversion serves 256 query rows.  With 128 rows or fewer (a "narrow"
+// segment) both warpgroups take the same rows and alternate chunks, and the
+// first one folds the second's result in at the end.
+// Registers: 512 threads start with 128 each; the softmax warpgroups take 176,
+// the conversion keeps 104, the issuing group 56 (their sum is what the block has).
+// Every wait is bounded (XGR_DEV_TIMEOUT and an unwound CTA, no hang).
+#include "cache_codes.cuh"
+#include "cache_plan.cuh"
+#include "tcgen.cuh"
+
+namespace xgr {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kConvThreads = 128;
+constexpr int kChunk = 128;                    // keys of a chunk
+constexpr int kRing = 4;                       // chunks whose scales are at hand
+constexpr uint32_t kTmemCols = 512;            // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512)
+constexpr float kMinLogV = -100.f;             // log2 of the smallest V scale told from 0
+
+struct Scales {
+    float k[8], lv[8], iv[8];   // by 16 keys: K scale, log2 V scale, 1 / V scale
+    int bad;                    // bit g: group g lies in a page that is not there; bit 8: a V scale is NaN
+    int pad[3];
+};
+
+template <int D>
+struct Lay {
+    static constexpr uint32_t kHalf = 16384;                  // 128 rows x 64 fp16
+    static constexpr uint32_t kTile = 128 * D * 2;
+    static constexpr uint32_t q = 0;                          // two tiles
+    static constexpr uint32_t k = 2 * kTile;                  // two stages
+    static constexpr uint32_t v = 4 * kTile;
+    static constexpr uint32_t sc = 6 * kTile;
+    static constexpr uint32_t x = sc + kRing * sizeof(Scales);   // [128] (M, l) of a narrow segment's second half
+    static constexpr uint32_t bar = x + 1024;
+    static constexpr uint32_t misc = bar + 256;
+    static constexpr uint32_t total = misc + 16 + 1024;       // with room to align the window
+};
+
+enum { B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_SFULL = 8, B_PFULL = 10, B_PVDONE = 12, B_QFULL = 14,
+       B_SC = 16, B_XCH = B_SC + kRing, B_XDONE, B_DONE, B_COUNT };
+static_assert(B_COUNT * 8 <= 256, "barrier area");
+
+// byte offset of 16-byte chunk c of row `row` in a 128-row operand of 64-column swizzled halves
+template <int D>
+__device__ __forceinline__ uint32_t sw128(int row, int c) {
+    return (uint32_t)(c >> 3) * Lay<D>::kHalf + (uint32_t)row * 128u + (uint32_t)(((c & 7) ^ (row & 7)) << 4);
+}
+
+// A segment as every role sees it.
+struct Seg {
+    RowSpan row;
+    int u1, kb0, ke, chunks, rows;
+    bool narrow;
+    __device__ int tile_chunks(int h) const {   // chunks of S_h
+        return narrow ? (chunks + 1 - h) / 2 : h == 0 || rows > 128 ? chunks : 0;
+    }
+    __device__ int chunk_of(int h, int i) const { return narrow ? 2 * i + h : i; }
+};
+
+__device__ __forceinline__ Seg segment(const AttendArgs &a, const Cursor &cur, int64_t left) {
+    constexpr int R = 256;
+    Seg s;
+    s.row = row_span(a.c, cur.r, a.max_q);
+    s.u1 = (int)min((int64_t)cur.units, cur.u + left);
+    const KeyRange k = segment_keys(a, s.row, cur, s.u1, R);
+    s.kb0 = k.lo & ~(kChunk - 1);
+    s.ke = k.hi;
+    s.chunks = k.hi > k.lo ? (k.hi - s.kb0 + kChunk - 1) / kChunk : 0;
+    s.rows = min(R, s.row.n * a.G - cur.t * R);
+    s.narrow = s.rows <= 128;
+    return s;
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs a, PlanOut po, int min_units) {
+    using L = Lay<D>;
+    constexpr int R = 256;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(base);
+    auto bar = [&](int i) { return sb + L::bar + 8u * (uint32_t)i; };
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(base + L::misc);
+    volatile int *abort = reinterpret_cast<int *>(base + L::misc + 4);
+    Scales *ring = reinterpret_cast<Scales *>(base + L::sc);
+    float2 *xch = reinterpret_cast<float2 *>(base + L::x);
+    const CacheArgs &c = a.c;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_KFULL + i), kConvThreads);
+            mbar_init(bar(B_VFULL + i), kConvThreads);
+            mbar_init(bar(B_KEMPTY + i), 2);      // a commit for each tile (two for a chunk of one tile)
+            mbar_init(bar(B_VEMPTY + i), 2);
+            mbar_init(bar(B_SFULL + i), 1);
+            mbar_init(bar(B_PFULL + i), 128);
+            mbar_init(bar(B_PVDONE + i), 1);
+            mbar_init(bar(B_QFULL + i), 128);
+        }
+        for (int i = 0; i < kRing; ++i) mbar_init(bar(B_SC + i), 1);
+        mbar_init(bar(B_XCH), 128);
+        mbar_init(bar(B_XDONE), 128);
+        mbar_init(bar(B_DONE), 1);
+        *abort = 0;
+        fence_mbar_init();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    Cursor cur;
+    int64_t begin, end, per;
+    if (!plan_begin<kThreads>(a, R, min_units, po, cur, begin, end, per)) return;   // (of the whole block)
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        tc::regs_up<176>();
+        const int h = warp / 4;
+        const int tr = tid % 128;                                     // row of the tile, TMEM lane
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + 128u * h + lanes, to = tmem + 256u + 128u * h + lanes;
+        const bool capped = a.softcap > 0.f;
+        int gc = 0;        // chunks of the segments before
+        int cnt = 0;       // of them, this warpgroup's
+        int nx = 0;        // narrow segments before
+        bool ok = true;
+        for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
+            const Seg s = segment(a, cur, end - at);
+            const int ia = cur.t * R + tr + (s.narrow ? 0 : 128 * h);
+            const bool valid = ia < s.row.n * a.G;
+            const int tok = valid ? ia / a.G : 0, head = cur.g * a.G + (valid ? ia % a.G : 0);
+            KeyRange vis = query_keys(a, s.row, cur.r, tok);
+            if (!valid) vis = KeyRange{0, 0x7fffffff};                // a row of zeros, never written
+            const int n = s.tile_chunks(h);
+            const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
+            const int pos = s.row.len - s.row.n + tok;
+            // ---- the query row as fp16, near 1
+            float fac = 0.f;
+            if (n > 0 || (s.narrow && s.chunks > 0)) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (int64_t)(s.row.t0 + tok) * a.q_stride +
+                                                                   (int64_t)head * D);
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    float f[8];
+                    unpack8(valid ? src[i] : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+                }
+                const int ex = query_exp(top);
+                fac = a.scale * pow2i(ex);
+                if (!s.narrow || h == 0) {
+                    const float down = pow2i(-ex);
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        float f[8];
+                        unpack8(valid ? src[i] : make_uint4(0, 0, 0, 0), f);
+                        *reinterpret_cast<uint4 *>(base + L::q + h * L::kTile + sw128<D>(tr, i)) =
+                            make_uint4(pack_f16(f[0] * down, f[1] * down), pack_f16(f[2] * down, f[3] * down),
+                                       pack_f16(f[4] * down, f[5] * down), pack_f16(f[6] * down, f[7] * down));
+                    }
+                    fence_async_smem();
+                    mbar_arrive(bar(B_QFULL + h));
+                }
+            }
+            // what one factor can hold of a score's way to log2 units
+            const float f0 = capped ? fac * (2.f * kLog2e / a.softcap) : fac * kLog2e;
+            const int lo_max = __reduce_max_sync(0xffffffffu, valid ? vis.lo : 0);
+            const int hi_min = __reduce_min_sync(0xffffffffu, vis.hi);
+
+            float M = -INFINITY, l = 0.f;
+            for (int i = 0; i < n; ++i) {
+                const int ch = s.chunk_of(h, i), gi = gc + ch;
+                ok = mbar_wait(bar(B_SC + gi % kRing), (gi / kRing) & 1, abort) &&
+                     mbar_wait(bar(B_SFULL + h), (cnt + i) & 1, abort);
+                if (!ok) break;
+                tc::fence_after();
+                float x[128];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) tc::ld32(ts + 32u * p, x + 32 * p);
+                const Scales &sc = ring[gi % kRing];
+                const int key0 = s.kb0 + ch * kChunk;
+                const int bad = sc.bad;
+                const bool masked = key0 < lo_max || key0 + kChunk > hi_min || bad;
+                const bool slow = masked || capped || a.slopes;
+                float f[8], lv[8];
+#pragma unroll
+                for (int g = 0; g < 8; g += 4) {
+                    const float4 kk = *reinterpret_cast<const float4 *>(&sc.k[g]);
+                    const float4 vv = *reinterpret_cast<const float4 *>(&sc.lv[g]);
+                    f[g] = kk.x * f0; f[g + 1] = kk.y * f0; f[g + 2] = kk.z * f0; f[g + 3] = kk.w * f0;
+                    lv[g] = vv.x; lv[g + 1] = vv.y; lv[g + 2] = vv.z; lv[g + 3] = vv.w;
+                }
+#pragma unroll
+                for (int p = 0; p < 4; ++p) tc::wait_ld_into(x + 32 * p);
+                if (slow) {
+                    const float up = a.softcap * kLog2e;
+                    const float away = (float)(pos - key0);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int r0 = vis.lo - key0 - 32 * p, r1 = vis.hi - key0 - 32 * p;
+                        const uint32_t below = r0 >= 32 ? ~0u : r0 <= 0 ? 0u : (1u << r0) - 1u;
+                        const uint32_t till = r1 >= 32 ? ~0u : r1 <= 0 ? 0u : (1u << r1) - 1u;
+                        uint32_t seen = till & ~below;
+                        if (bad >> (2 * p) & 1) seen &= 0xffff0000u;
+                        if (bad >> (2 * p + 1) & 1) seen &= 0x0000ffffu;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float y = x[32 * p + e] * f[2 * p + e / 16];
+                            if (capped) y = up * tanh_score(y);
+                            if (a.slopes) y -= slope * fabsf(away - (float)(32 * p + e));
+                            x[32 * p + e] = seen >> e & 1 ? y : -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) f[g] = 1.f;
+                }
+                // ---- the largest weight's exponent, the row's reference
+                float top = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    float m = fmaxf(x[16 * g], x[16 * g + 1]);
+#pragma unroll
+                    for (int e = 2; e < 16; e += 2) m = tc::fmax3(m, x[16 * g + e], x[16 * g + e + 1]);
+                    top = fmaxf(top, fmaf(m, f[g], lv[g]));
+                }
+                const bool raise = top > M + 8.f || (M == -INFINITY && top > -INFINITY);
+                float alpha = 1.f;
+                if (raise) {
+                    alpha = exp2_fast(M - top);
+                    M = top;
+                    l *= alpha;
+                }
+                if (i > 0 && __any_sync(0xffffffffu, raise)) {   // O_h holds every product so far: S_h waited for them
+#pragma unroll 1
+                    for (int p = 0; p < D / 32; ++p) {
+                        float o[32];
+                        tc::ld32(to + 32u * p, o);
+                        tc::wait_ld_into(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tc::st32(to + 32u * p, reinterpret_cast<const uint32_t *>(o));
+                    }
+                }
+                // ---- the weights
+                const float ref = (M == -INFINITY ? 0.f : M) - kTcBias;
+                uint32_t w[64];
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const float2 ff = make_float2(f[g], f[g]), dd = make_float2(lv[g] - ref, lv[g] - ref);
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 t = tc::ffma2(make_float2(x[16 * g + e], x[16 * g + e + 1]), ff, dd);
+                        float p0 = exp2_fast(t.x), p1 = exp2_fast(t.y);
+                        if (slow && bad >> 8) {   // a NaN scale: keys that are not seen weigh 0 all the same
+                            if (x[16 * g + e] == -INFINITY) p0 = 0.f;
+                            if (x[16 * g + e + 1] == -INFINITY) p1 = 0.f;
+                        }
+                        s0 += p0;
+                        s1 += p1;
+                        w[8 * g + e / 2] = pack_f16(p0, p1);
+                    }
+                    s0 += s1;
+                    l += s0 == 0.f ? 0.f : s0 * sc.iv[g];
+                }
+                __syncwarp();
+                tc::st32(ts, w);
+                tc::st32(ts + 32u, w + 32);
+                tc::wait_st();
+                tc::fence_before();
+                mbar_arrive(bar(B_PFULL + h));
+            }
+            // ---- the segment's result
+            if (ok && n > 0) ok = mbar_wait(bar(B_PVDONE + h), (cnt + n - 1) & 1, abort);
+            cnt += n;
+            gc += s.chunks;
+            bool fold = false;   // a narrow segment's second half is folded in
+            float a0 = 1.f, a1 = 0.f;
+            if (ok && s.narrow && s.chunks > 1) {
+                if (h == 1) {
+                    tc::fence_before();
+                    xch[tr] = make_float2(M, l);
+                    mbar_arrive(bar(B_XCH));
+                    ok = mbar_wait(bar(B_XDONE), nx & 1, abort);   // O_1 and xch are read
+                } else {
+                    ok = mbar_wait(bar(B_XCH), nx & 1, abort);
+                    const float2 y = xch[tr];
+                    const float m = fmaxf(M, y.x), ref = m == -INFINITY ? 0.f : m;
+                    a0 = exp2_fast(M - ref);
+                    a1 = exp2_fast(y.x - ref);
+                    l = l * a0 + y.y * a1;
+                    M = m;
+                    fold = true;
+                }
+                ++nx;
+            }
+            if (!ok) break;
+            if (!s.narrow || h == 0) {
+                tc::fence_after();
+                const bool all = cur.u == 0 && s.u1 == cur.units;
+                const int64_t oi = (int64_t)(s.row.t0 + tok) * a.Hq + head;
+                const int64_t pi = ((int64_t)blockIdx.x * 2 + (cur.u == 0 ? 1 : 0)) * R + tr + 128 * h;
+                const float ref = M == -INFINITY ? 0.f : M;
+                const float scale = !all ? 1.f : l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+                for (int p = 0; p < D / 32; ++p) {
+                    float o[32];
+                    __syncwarp();
+                    if (n > 0) {
+                        tc::ld32(to + 32u * p, o);
+                        tc::wait_ld_into(o);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    }
+                    if (fold) {
+                        float o1[32];
+                        tc::ld32(to + 128u + 32u * p, o1);
+                        tc::wait_ld_into(o1);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = o[e] * a0 + o1[e] * a1;
+                    }
+                    if (valid && all) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + oi * D + 32 * p);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint4 pk;
+                            __nv_bfloat162 *b = reinterpret_cast<__nv_bfloat162 *>(&pk);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                b[j] = __floats2bfloat162_rn(o[8 * e + 2 * j] * scale, o[8 * e + 2 * j + 1] * scale);
+                            dst[e] = pk;
+                        }
+                    } else if (valid) {
+                        float4 *dst = reinterpret_cast<float4 *>(po.o + pi * D + 32 * p);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+                if (valid) {
+                    if (all) a.lse[oi] = l == 0.f ? -INFINITY : (ref - kTcBias + log2f(l)) * kLn2;
+                    else po.ml[pi] = make_float2(M, l);
+                }
+                tc::fence_before();
+                if (fold) mbar_arrive(bar(B_XDONE));
+            }
+            at += s.u1 - cur.u;
+            if (at < end) plan_next(a, R, cur);
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ codes to operands
+        tc::regs_down<104>();
+        const int t = tid - 256;
+        // lane -> (key, 16-byte chunk) of a group of 16 keys, so that eight lanes' 16-byte writes meet no bank twice
+        constexpr int kCh = D / 16;                                // chunks of a key
+        const int ck = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
+        const int kr = D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
+        constexpr int kRows = 128 / kCh;                           // keys of one pass of the 128 threads
+        constexpr int kPass = kChunk / kRows;
+        const int key_in = (t / 32) * (32 / kCh) + kr;             // key of the pass
+        int gc = 0;
+        bool ok = true;
+        for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
+            const Seg s = segment(a, cur, end - at);
+            const int32_t *line = c.table + (int64_t)cur.r * c.max_pages;
+            // lane g of every warp holds the page of group g % 8 of a chunk (-2: no keys, -1: no such page)
+            auto ids_of = [&](int ch) {
+                const int key = s.kb0 + ch * kChunk + 16 * (lane & 7);
+                int id = -2;
+                if (ch < s.chunks && key < s.ke) {
+                    id = line[key >> c.page_shift];
+                    if (id < 0 || id >= c.n_pages) {
+                        if (t == lane) set_status(c.status, XGR_DEV_INDEX);
+                        id = -1;
+                    }
+                }
+                return id;
+            };
+            auto load = [&](const uint8_t *src, int ch, int ids, uint4 *v) {
+#pragma unroll
+                for (int i = 0; i < kPass; ++i) {
+                    const int kl = i * kRows + key_in;
+                    const int key = s.kb0 + ch * kChunk + kl;
+                    const int id = __shfl_sync(0xffffffffu, ids, kl / 16);
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (id >= 0 && key < s.ke)
+                        v[i] = __ldg(reinterpret_cast<const uint4 *>(
+                            src + (((int64_t)id * c.Hkv + cur.g) * c.page + (key & (c.page - 1))) * D + ck * 16));
+                }
+            };
+            auto put = [&](uint32_t off, const uint4 *v) {
+#pragma unroll
+                for (int i = 0; i < kPass; ++i) {
+                    const int kl = i * kRows + key_in;
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) codes_to_f16<FMT>(w[e], o[2 * e], o[2 * e + 1]);
+                    *reinterpret_cast<uint4 *>(base + off + sw128<D>(kl, 2 * ck)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(base + off + sw128<D>(kl, 2 * ck + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                fence_async_smem();
+            };
+            uint4 kv[kPass], vv[kPass];
+            int ids = ids_of(0), next = ids_of(1);
+            if (s.chunks > 0) {
+                load(c.k, 0, ids, kv);
+                load(c.v, 0, ids, vv);
+            }
+            for (int ch = 0; ch < s.chunks; ++ch) {
+                const int gi = gc + ch, st = gi & 1;
+                const int ids2 = next;
+                next = ids_of(ch + 2);
+                if (gi >= 2) ok = mbar_wait(bar(B_KEMPTY + st), ((gi >> 1) - 1) & 1, abort);
+                if (!ok) break;
+                // (S of chunk gi - 2 is complete, so the softmax is done with the scales of chunk gi - 4)
+                if (t < 32) {   // the chunk's scales
+                    float ks = 0.f, vs = 0.f;
+                    if (ids >= 0) {
+                        const int64_t at_s = (int64_t)ids * c.Hkv + cur.g;
+                        ks = clean_scale(c.ks[at_s]);
+                        vs = clean_scale(c.vs[at_s]);
+                    }
+                    const float lv = vs != vs ? vs : fmaxf(log2f(vs), kMinLogV);
+                    Scales &sc = ring[gi % kRing];
+                    const uint32_t gone = __ballot_sync(0xffffffffu, ids == -1) & 255u;
+                    const uint32_t sick = __ballot_sync(0xffffffffu, vs != vs || ks != ks) & 255u;
+                    if (lane < 8) {
+                        sc.k[lane] = ks;
+                        sc.lv[lane] = lv;
+                        sc.iv[lane] = exp2f(-lv);
+                    }
+                    if (lane == 0) sc.bad = (int)gone | (sick ? 256 : 0);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_SC + gi % kRing));
+                }
+                put(L::k + st * L::kTile, kv);
+                mbar_arrive(bar(B_KFULL + st));
+                if (ch + 1 < s.chunks) load(c.k, ch + 1, ids2, kv);
+                if (gi >= 2) ok = mbar_wait(bar(B_VEMPTY + st), ((gi >> 1) - 1) & 1, abort);
+                if (!ok) break;
+                put(L::v + st * L::kTile, vv);
+                mbar_arrive(bar(B_VFULL + st));
+                if (ch + 1 < s.chunks) load(c.v, ch + 1, ids2, vv);
+                ids = ids2;
+            }
+            gc += s.chunks;
+            at += s.u1 - cur.u;
+            if (at < end) plan_next(a, R, cur);
+        }
+    } else {
+        // ------------------------------------------------------------ products
+        tc::regs_down<56>();
+        if (warp == 12) {
+            constexpr uint32_t idS = tc::idesc_f16(128, 128, false), idO = tc::idesc_f16(128, D, true);
+            int gc = 0, cnt0 = 0, cnt1 = 0, nq0 = 0, nq1 = 0;
+            bool ok = true;
+            for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
+                const Seg s = segment(a, cur, end - at);
+                if (lane == 0 && s.chunks > 0) {
+                    const int n[2] = {s.tile_chunks(0), s.tile_chunks(1)};
+                    const int cnt[2] = {cnt0, cnt1};
+                    // the buffers of the segment before are free
+                    if (cnt0 > 0) ok = mbar_wait(bar(B_PVDONE), (cnt0 - 1) & 1, abort);
+                    if (ok && cnt1 > 0) ok = mbar_wait(bar(B_PVDONE + 1), (cnt1 - 1) & 1, abort);
+                    if (ok) ok = mbar_wait(bar(B_QFULL), nq0 & 1, abort);
+                    if (ok && n[1] > 0 && !s.narrow) ok = mbar_wait(bar(B_QFULL + 1), nq1 & 1, abort);
+                    const bool alone = s.narrow || n[1] == 0;   // a chunk feeds one tile: it commits for both
+                    int is[2] = {0, 0}, ip[2] = {0, 0};
+                    uint32_t idle = 0;
+                    while (ok && (ip[0] < n[0] || ip[1] < n[1])) {
+                        bool progress = false;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (ip[h] < is[h]) {   // O_h += W_h V
+                                const int gi = gc + s.chunk_of(h, ip[h]), st = gi & 1;
+                                if (mbar_test(bar(B_PFULL + h), (cnt[h] + ip[h]) & 1) &&
+                                    mbar_test(bar(B_VFULL + st), (gi >> 1) & 1)) {
+                                    tc::fence_after();
+                                    const uint32_t kv = sb + L::v + st * L::kTile;
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k)
+                                        tc::mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 8u * k,
+                                                   tc::desc(kv + (uint32_t)k * 2048u, L::kHalf, 1024), idO,
+                                                   (k > 0 || ip[h] > 0) ? 1u : 0u);
+                                    tc::commit(bar(B_PVDONE + h));
+                                    tc::commit(bar(B_VEMPTY + st));
+                                    if (alone) tc::commit(bar(B_VEMPTY + st));
+                                    ++ip[h];
+                                    progress = true;
+                                }
+                            }
+                            if (is[h] < n[h] && is[h] == ip[h] &&
+                                (is[h] == 0 || mbar_test(bar(B_PVDONE + h), (cnt[h] + is[h] - 1) & 1))) {   // S_h = Q_h K^T
+                                const int gi = gc + s.chunk_of(h, is[h]), st = gi & 1;
+                                if (mbar_test(bar(B_KFULL + st), (gi >> 1) & 1)) {
+                                    tc::fence_after();
+                                    const uint32_t kq = sb + L::q + (s.narrow ? 0 : h) * L::kTile;
+                                    const uint32_t kk = sb + L::k + st * L::kTile;
+#pragma unroll
+                                    for (int k = 0; k < D / 16; ++k) {
+                                        const uint32_t off = (uint32_t)(k >> 2) * L::kHalf + (uint32_t)(k & 3) * 32u;
+                                        tc::mma_ss(tmem + 128u * h, tc::desc(kq + off, 16, 1024),
+                                                   tc::desc(kk + off, 16, 1024), idS, k > 0);
+                                    }
+                                    tc::commit(bar(B_SFULL + h));
+                                    tc::commit(bar(B_KEMPTY + st));
+                                    if (alone) tc::commit(bar(B_KEMPTY + st));
+                                    ++is[h];
+                                    progress = true;
+                                }
+                            }
+                        }
+                        if (progress) {
+                            idle = 0;
+                        } else if (++idle >= kSpinLimit) {
+                            *abort = 1;
+                            ok = false;
+                        } else if ((idle & 255) == 0 && *abort) {
+                            ok = false;
+                        }
+                    }
+                    cnt0 += n[0];
+                    cnt1 += n[1];
+                    ++nq0;
+                    if (!s.narrow && n[1] > 0) ++nq1;
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                gc += s.chunks;
+                at += s.u1 - cur.u;
+                if (at < end) plan_next(a, R, cur);
+            }
+            if (lane == 0) {   // every product issued has completed before tensor memory is given back
+                tc::commit(bar(B_DONE));
+                mbar_wait(bar(B_DONE), 0, nullptr);
+            }
+            __syncwarp();
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort) set_status(c.status, XGR_DEV_TIMEOUT);
+    if (warp == 12) {
+        tc::fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+template <int D, int FMT>
+cudaError_t launch_t(const AttendArgs &a, const PlanOut &po, int ctas, int min_units, cudaStream_t s) {
+    static bool ready[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, cache_attend_tc_kernel<D, FMT>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;   // the warpgroups share out 512 x 128
+        e = cudaFuncSetAttribute(cache_attend_tc_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)Lay<D>::total);
+        if (e != cudaSuccess) return e;
+        ready[dev] = true;
+    }
+    return launch_pdl(cache_attend_tc_kernel<D, FMT>, dim3(ctas), dim3(kThreads), Lay<D>::total, s, a, po, min_units);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tc(const AttendArgs &a, const PlanOut &po, int ctas, int min_units, cudaStream_t s) {
+    if (a.c.D == 128)
+        return a.c.fmt == XGR_CACHE_E4M3 ? launch_t<128, XGR_CACHE_E4M3>(a, po, ctas, min_units, s)
+                                         : launch_t<128, XGR_CACHE_INT8>(a, po, ctas, min_units, s);
+    return a.c.fmt == XGR_CACHE_E4M3 ? launch_t<64, XGR_CACHE_E4M3>(a, po, ctas, min_units, s)
+                                     : launch_t<64, XGR_CACHE_INT8>(a, po, ctas, min_units, s);
+}
+
+}  // namespace xgr

@@ -53,18 +53,14 @@ __device__ __forceinline__ int range_units(const AttendArgs &a, const KeyRange &
     return max(1, (k.hi + kUnitKeys - 1) / kUnitKeys - k.lo / kUnitKeys);
 }
 
-// Rows whose query rows lie in (min_rows, max_rows] are this kernel's.
-struct RowsOf {
-    int min_rows, max_rows, R;
-    __device__ bool mine(int64_t rows) const { return rows > min_rows && rows <= max_rows; }
-};
+__device__ __forceinline__ int row_tiles(const AttendArgs &a, const RowSpan &s, int R) {
+    return (int)(((int64_t)s.n * a.G + R - 1) / R);
+}
 
-__device__ __forceinline__ int64_t row_units(const AttendArgs &a, const RowSpan &s, int r, const RowsOf &w) {
-    const int64_t rows = (int64_t)s.n * a.G;
-    if (s.n == 0 || !w.mine(rows)) return 0;
-    const int tiles = (int)((rows + w.R - 1) / w.R);
+__device__ __forceinline__ int64_t row_units(const AttendArgs &a, const RowSpan &s, int r, int R) {
+    const int tiles = row_tiles(a, s, R);
     int64_t u = 0;
-    for (int t = 0; t < tiles; ++t) u += range_units(a, tile_keys(a, s, r, w.R, t));
+    for (int t = 0; t < tiles; ++t) u += range_units(a, tile_keys(a, s, r, R, t));
     return u * a.c.Hkv;
 }
 
@@ -78,7 +74,7 @@ struct Cursor {
 // Every thread of the block gets the block's first cursor and [begin, end)
 // (false: no work).  T = threads of the block.
 template <int T>
-__device__ __forceinline__ bool plan_begin(const AttendArgs &a, const RowsOf &w, int min_units,
+__device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_units,
                                            const PlanOut &p, Cursor &cur, int64_t &begin, int64_t &end,
                                            int64_t &per) {
     __shared__ int64_t base[T / 32 + 1];
@@ -88,7 +84,7 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, const RowsOf &w,
     const int r0 = min((int)threadIdx.x * rpt, n_rows), r1 = min(r0 + rpt, n_rows);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += row_units(a, row_span(a.c, r, a.max_q), r, w);
+    for (int r = r0; r < r1; ++r) mine += row_units(a, row_span(a.c, r, a.max_q), r, R);
     int64_t x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -110,7 +106,7 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, const RowsOf &w,
         int64_t at = from;
         for (int r = r0; r < r1; ++r) {
             p.row_unit[r] = at;
-            at += row_units(a, row_span(a.c, r, a.max_q), r, w);
+            at += row_units(a, row_span(a.c, r, a.max_q), r, R);
         }
         if (threadIdx.x == 0) *p.per = per;
     }
@@ -119,15 +115,15 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, const RowsOf &w,
         int64_t left = begin - from;
         int r = r0;
         for (; r < r1 - 1; ++r) {
-            const int64_t u = row_units(a, row_span(a.c, r, a.max_q), r, w);
+            const int64_t u = row_units(a, row_span(a.c, r, a.max_q), r, R);
             if (left < u) break;
             left -= u;
         }
         const RowSpan s = row_span(a.c, r, a.max_q);
-        const int tiles = (int)(((int64_t)s.n * a.G + w.R - 1) / w.R);
+        const int tiles = row_tiles(a, s, R);
         int t = 0, units = 1;
         for (; t < tiles; ++t) {
-            units = range_units(a, tile_keys(a, s, r, w.R, t));
+            units = range_units(a, tile_keys(a, s, r, R, t));
             if (left < (int64_t)units * a.c.Hkv) break;
             left -= (int64_t)units * a.c.Hkv;
         }
@@ -143,16 +139,15 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, const RowsOf &w,
 }
 
 // The segment after cur; cur.r = n_rows behind the last one.
-__device__ __forceinline__ void plan_next(const AttendArgs &a, const RowsOf &w, Cursor &cur) {
+__device__ __forceinline__ void plan_next(const AttendArgs &a, int R, Cursor &cur) {
     cur.u = 0;
     if (++cur.g < a.c.Hkv) return;
     cur.g = 0;
     ++cur.t;
     for (; cur.r < a.c.n_rows; ++cur.r, cur.t = 0) {
         const RowSpan s = row_span(a.c, cur.r, a.max_q);
-        const int64_t rows = (int64_t)s.n * a.G;
-        if (s.n == 0 || !w.mine(rows) || (int64_t)cur.t * w.R >= rows) continue;
-        cur.units = range_units(a, tile_keys(a, s, cur.r, w.R, cur.t));
+        if (cur.t >= row_tiles(a, s, R)) continue;
+        cur.units = range_units(a, tile_keys(a, s, cur.r, R, cur.t));
         return;
     }
 }
@@ -167,6 +162,27 @@ __device__ __forceinline__ KeyRange query_keys(const AttendArgs &a, const RowSpa
     }
     if (a.window > 0) k.lo = max(0, pos - a.window + 1);
     if (a.first) k.lo = max(k.lo, a.first[s.t0 + i]);
+    return k;
+}
+
+// The keys [kb, ke) of units [cur.u, u1) of segment cur that some query of its
+// tile sees (empty: none), worked out by a whole warp.
+__device__ __forceinline__ KeyRange segment_keys(const AttendArgs &a, const RowSpan &s, const Cursor &cur, int u1,
+                                                 int R) {
+    KeyRange k = tile_keys(a, s, cur.r, R, cur.t);
+    if (!a.whole) {
+        const int unit0 = k.lo / kUnitKeys;
+        k = KeyRange{max(k.lo, (unit0 + cur.u) * kUnitKeys), min(k.hi, (unit0 + u1) * kUnitKeys)};
+    }
+    if (a.first) {
+        const int i0 = cur.t * R / a.G, i1 = (min((cur.t + 1) * R, s.n * a.G) - 1) / a.G;
+        int lo = 0x7fffffff;
+        for (int i = i0 + (int)(threadIdx.x % 32); i <= i1; i += 32) {
+            const KeyRange q = query_keys(a, s, cur.r, i);
+            if (q.lo < q.hi) lo = min(lo, q.lo);
+        }
+        k.lo = max(k.lo, __reduce_min_sync(0xffffffffu, lo));
+    }
     return k;
 }
 
@@ -192,5 +208,9 @@ __device__ __forceinline__ float clean_scale(float s) {
 // The weights are kept as 2^14 p (fp16 in the products): p <= 1 leaves the top
 // of fp16's range, so a weight as small as 2^-38 of the row's largest still counts.
 constexpr float kBias = 14.f;
+constexpr float kTcBias = 7.f;   // of the tcgen05 kernel, whose reference lags by up to 2^8
+
+// cache_attend_tc.cu: 256-row tiles, one CTA an SM
+cudaError_t launch_attend_tc(const AttendArgs &a, const PlanOut &po, int ctas, int min_units, cudaStream_t s);
 
 }  // namespace xgr

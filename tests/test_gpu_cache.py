@@ -474,7 +474,6 @@ def test_fork_is_exact(seed):
     cache = random_cache(rng, pages, 1 + seed % 3, page, d, fmt)
     table, lens = shared_tables(rng, pages, page, width, n_rows)
     pc = to_device(cache)
-    status = 0
     for step in range(4):
         n_out = int(rng.integers(1, 50))
         parent = rng.integers(-1, len(lens), n_out).astype(np.int32)
@@ -485,9 +484,7 @@ def test_fork_is_exact(seed):
         assert np.array_equal(t2.cpu().numpy(), want_t) and np.array_equal(l2.cpu().numpy(), want_l)
         same_cache(to_host(pc), cache)
         assert pc.device_status() == st
-        status |= st
         table, lens = want_t, want_l
-    return status
 
 
 def test_fork_many_pages_and_rows():

@@ -55,18 +55,10 @@ struct Smem {
     int bad[kWarps][kStages];                                  // bit h: half h lies in a page that is not there
     float m[kWarps][16 * MT], l[kWarps][16 * MT];
     float vref[kWarps];
+    PlanSmem<kThreads> plan;
     alignas(16) uint32_t qf[MT > 1 ? MT * (D / 16) * 128 : 4];  // query fragments (MT > 1; else in registers)
     static_assert(16 * MT * D * 4 <= kStages * kStageBytes, "the O buffer fits the rings");
 };
-
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0)
-                 : "memory");
-}
 
 __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -93,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
     griddep_launch_dependents();
     Cursor cur;
     int64_t begin, end, per;
-    if (!plan_begin<kThreads>(a, R, min_units, po, cur, begin, end, per)) return;
+    if (!plan_begin<kThreads>(a, R, min_units, sm.plan, po, cur, begin, end, per)) return;
 
     const uint32_t ring0 = smem_u32(&sm.ring[warp][0][0]);
     const uint32_t sc0 = smem_u32(&sm.sc[warp][0][0]);

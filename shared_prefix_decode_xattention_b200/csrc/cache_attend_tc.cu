@@ -15,17 +15,17 @@
 //   warps 0-7    two softmax warpgroups, a query row a thread: scores from
 //                tensor memory, cap, bias, mask, weights back over the scores'
 //                buffer as fp16, and at a segment's end the output;
-//   warps 8-11   the codes of each 128-key chunk, 16 bytes a load straight from
-//                the pages into registers one chunk ahead, converted and written
-//                as the 128-byte-swizzled operands of K and V (rings of two);
+//   warps 8-11   the codes of each 128-key chunk, 16 bytes a copy from the pages
+//                one chunk ahead, converted and written as the
+//                128-byte-swizzled operands of K and V (rings of two);
 //   warp 12      issues the products: S_h = Q_h K^T, O_h += W_h V, whichever of
 //                the two tiles is ready, so one tile's softmax runs beside the
 //                other's products.
 // A conversion serves 256 query rows.  With 128 rows or fewer (a "narrow"
 // segment) both warpgroups take the same rows and alternate chunks, and the
 // first one folds the second's result in at the end.
-// Registers: 512 threads start with 128 each; the softmax warpgroups take 176,
-// the conversion keeps 104, the issuing group 56 (their sum is what the block has).
+// Registers: 512 threads start with 128 each; the softmax warpgroups take 192,
+// the conversion and the issuing group keep 64 (their sum is what the block has).
 // Every wait is bounded (XGR_DEV_TIMEOUT and an unwound CTA, no hang).
 #include "cache_codes.cuh"
 #include "cache_plan.cuh"
@@ -55,7 +55,8 @@ struct Lay {
     static constexpr uint32_t q = 0;                          // two tiles
     static constexpr uint32_t k = 2 * kTile;                  // two stages
     static constexpr uint32_t v = 4 * kTile;
-    static constexpr uint32_t sc = 6 * kTile;
+    static constexpr uint32_t raw = 6 * kTile;                // codes of the next K and V chunk (first the plan's scratch)
+    static constexpr uint32_t sc = raw + 2 * kChunk * D;
     static constexpr uint32_t x = sc + kRing * sizeof(Scales);   // [128] (M, l) of a narrow segment's second half
     static constexpr uint32_t bar = x + 1024;
     static constexpr uint32_t misc = bar + 256;
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
     griddep_launch_dependents();
     Cursor cur;
     int64_t begin, end, per;
-    if (!plan_begin<kThreads>(a, R, min_units, po, cur, begin, end, per)) return;   // (of the whole block)
+    if (!plan_begin<kThreads>(a, R, min_units, *reinterpret_cast<PlanSmem<kThreads> *>(base + L::raw), po, cur, begin, end, per)) return;   // (of the whole block)
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                      "r"(kTmemCols)
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
-        tc::regs_up<176>();
+        tc::regs_up<192>();
         const int h = warp / 4;
         const int tr = tid % 128;                                     // row of the tile, TMEM lane
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -217,14 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 const int bad = sc.bad;
                 const bool masked = key0 < lo_max || key0 + kChunk > hi_min || bad;
                 const bool slow = masked || capped || a.slopes;
-                float f[8], lv[8];
-#pragma unroll
-                for (int g = 0; g < 8; g += 4) {
-                    const float4 kk = *reinterpret_cast<const float4 *>(&sc.k[g]);
-                    const float4 vv = *reinterpret_cast<const float4 *>(&sc.lv[g]);
-                    f[g] = kk.x * f0; f[g + 1] = kk.y * f0; f[g + 2] = kk.z * f0; f[g + 3] = kk.w * f0;
-                    lv[g] = vv.x; lv[g + 1] = vv.y; lv[g + 2] = vv.z; lv[g + 3] = vv.w;
-                }
 #pragma unroll
                 for (int p = 0; p < 4; ++p) tc::wait_ld_into(x + 32 * p);
                 if (slow) {
@@ -236,19 +229,24 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                         const uint32_t below = r0 >= 32 ? ~0u : r0 <= 0 ? 0u : (1u << r0) - 1u;
                         const uint32_t till = r1 >= 32 ? ~0u : r1 <= 0 ? 0u : (1u << r1) - 1u;
                         uint32_t seen = till & ~below;
+                        float2 kk = *reinterpret_cast<const float2 *>(&sc.k[2 * p]);
+                        kk.x *= f0;
+                        kk.y *= f0;
+                        const float2 vv = *reinterpret_cast<const float2 *>(&sc.lv[2 * p]);
                         if (bad >> (2 * p) & 1) seen &= 0xffff0000u;
                         if (bad >> (2 * p + 1) & 1) seen &= 0x0000ffffu;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            float y = x[32 * p + e] * f[2 * p + e / 16];
+                            float y = x[32 * p + e] * (e < 16 ? kk.x : kk.y);
                             if (capped) y = up * tanh_score(y);
                             if (a.slopes) y -= slope * fabsf(away - (float)(32 * p + e));
-                            x[32 * p + e] = seen >> e & 1 ? y : -INFINITY;
+                            x[32 * p + e] = seen >> e & 1 ? y + (e < 16 ? vv.x : vv.y) : -INFINITY;
                         }
                     }
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) f[g] = 1.f;
                 }
+                // t = factor * x + offset is a weight's exponent (x itself after the slow way)
+                auto factor = [&](int g) { return slow ? 1.f : sc.k[g] * f0; };
+                auto offset = [&](int g) { return slow ? 0.f : sc.lv[g]; };
                 // ---- the largest weight's exponent, the row's reference
                 float top = -INFINITY;
 #pragma unroll
@@ -256,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                     float m = fmaxf(x[16 * g], x[16 * g + 1]);
 #pragma unroll
                     for (int e = 2; e < 16; e += 2) m = tc::fmax3(m, x[16 * g + e], x[16 * g + e + 1]);
-                    top = fmaxf(top, fmaf(m, f[g], lv[g]));
+                    top = fmaxf(top, fmaf(m, factor(g), offset(g)));
                 }
                 const bool raise = top > M + 8.f || (M == -INFINITY && top > -INFINITY);
                 float alpha = 1.f;
@@ -278,29 +276,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 }
                 // ---- the weights
                 const float ref = (M == -INFINITY ? 0.f : M) - kTcBias;
-                uint32_t w[64];
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const float2 ff = make_float2(f[g], f[g]), dd = make_float2(lv[g] - ref, lv[g] - ref);
-                    float s0 = 0.f, s1 = 0.f;
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t w[32];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float2 t = tc::ffma2(make_float2(x[16 * g + e], x[16 * g + e + 1]), ff, dd);
-                        float p0 = exp2_fast(t.x), p1 = exp2_fast(t.y);
-                        if (slow && bad >> 8) {   // a NaN scale: keys that are not seen weigh 0 all the same
-                            if (x[16 * g + e] == -INFINITY) p0 = 0.f;
-                            if (x[16 * g + e + 1] == -INFINITY) p1 = 0.f;
+                    for (int g = 4 * q; g < 4 * q + 4; ++g) {
+                        const float fg = factor(g), dg = offset(g) - ref;
+                        const float2 ff = make_float2(fg, fg), dd = make_float2(dg, dg);
+                        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 t = tc::ffma2(make_float2(x[16 * g + e], x[16 * g + e + 1]), ff, dd);
+                            const float p0 = exp2_fast(t.x), p1 = exp2_fast(t.y);
+                            s0 += p0;
+                            s1 += p1;
+                            w[8 * (g & 3) + e / 2] = pack_f16(p0, p1);
                         }
-                        s0 += p0;
-                        s1 += p1;
-                        w[8 * g + e / 2] = pack_f16(p0, p1);
+                        s0 += s1;
+                        l += s0 == 0.f ? 0.f : s0 * sc.iv[g];
                     }
-                    s0 += s1;
-                    l += s0 == 0.f ? 0.f : s0 * sc.iv[g];
+                    __syncwarp();
+                    tc::st32(ts + 32u * q, w);
                 }
-                __syncwarp();
-                tc::st32(ts, w);
-                tc::st32(ts + 32u, w + 32);
                 tc::wait_st();
                 tc::fence_before();
                 mbar_arrive(bar(B_PFULL + h));
@@ -385,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------ codes to operands
-        tc::regs_down<104>();
+        tc::regs_down<64>();
         const int t = tid - 256;
         // lane -> (key, 16-byte chunk) of a group of 16 keys, so that eight lanes' 16-byte writes meet no bank twice
         constexpr int kCh = D / 16;                                // chunks of a key
@@ -412,23 +409,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 }
                 return id;
             };
-            auto load = [&](const uint8_t *src, int ch, int ids, uint4 *v) {
+            // a thread's codes wait in shared memory of its own (16 bytes of each pass)
+            const uint32_t raw = L::raw + 16u * t;
+            auto load = [&](const uint8_t *src, uint32_t to, int ch, int ids) {
+                if (ch < s.chunks) {
 #pragma unroll
-                for (int i = 0; i < kPass; ++i) {
-                    const int kl = i * kRows + key_in;
-                    const int key = s.kb0 + ch * kChunk + kl;
-                    const int id = __shfl_sync(0xffffffffu, ids, kl / 16);
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (id >= 0 && key < s.ke)
-                        v[i] = __ldg(reinterpret_cast<const uint4 *>(
-                            src + (((int64_t)id * c.Hkv + cur.g) * c.page + (key & (c.page - 1))) * D + ck * 16));
+                    for (int i = 0; i < kPass; ++i) {
+                        const int kl = i * kRows + key_in;
+                        const int key = s.kb0 + ch * kChunk + kl;
+                        const int id = __shfl_sync(0xffffffffu, ids, kl / 16);
+                        const bool in = id >= 0 && key < s.ke;
+                        const int64_t off = (((int64_t)id * c.Hkv + cur.g) * c.page + (key & (c.page - 1))) * D + ck * 16;
+                        cp_async16_zfill(sb + to + i * (kConvThreads * 16), src + (in ? off : 0), in);
+                    }
                 }
+                cp_async_commit();
             };
-            auto put = [&](uint32_t off, const uint4 *v) {
+            auto put = [&](uint32_t off, uint32_t from) {
 #pragma unroll
                 for (int i = 0; i < kPass; ++i) {
                     const int kl = i * kRows + key_in;
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    const uint4 v = *reinterpret_cast<const uint4 *>(base + from + i * (kConvThreads * 16));
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     uint32_t o[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) codes_to_f16<FMT>(w[e], o[2 * e], o[2 * e + 1]);
@@ -437,12 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 }
                 fence_async_smem();
             };
-            uint4 kv[kPass], vv[kPass];
+            const uint32_t raw_v = raw + kChunk * D;
             int ids = ids_of(0), next = ids_of(1);
-            if (s.chunks > 0) {
-                load(c.k, 0, ids, kv);
-                load(c.v, 0, ids, vv);
-            }
+            load(c.k, raw, 0, ids);
+            load(c.v, raw_v, 0, ids);
             for (int ch = 0; ch < s.chunks; ++ch) {
                 const int gi = gc + ch, st = gi & 1;
                 const int ids2 = next;
@@ -470,23 +470,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_SC + gi % kRing));
                 }
-                put(L::k + st * L::kTile, kv);
+                cp_async_wait_group<1>();
+                put(L::k + st * L::kTile, raw);
                 mbar_arrive(bar(B_KFULL + st));
-                if (ch + 1 < s.chunks) load(c.k, ch + 1, ids2, kv);
+                load(c.k, raw, ch + 1, ids2);
                 if (gi >= 2) ok = mbar_wait(bar(B_VEMPTY + st), ((gi >> 1) - 1) & 1, abort);
                 if (!ok) break;
-                put(L::v + st * L::kTile, vv);
+                cp_async_wait_group<1>();
+                put(L::v + st * L::kTile, raw_v);
                 mbar_arrive(bar(B_VFULL + st));
-                if (ch + 1 < s.chunks) load(c.v, ch + 1, ids2, vv);
+                load(c.v, raw_v, ch + 1, ids2);
                 ids = ids2;
             }
             gc += s.chunks;
             at += s.u1 - cur.u;
             if (at < end) plan_next(a, R, cur);
         }
+        cp_async_wait_all();
     } else {
         // ------------------------------------------------------------ products
-        tc::regs_down<56>();
+        tc::regs_down<64>();
         if (warp == 12) {
             constexpr uint32_t idS = tc::idesc_f16(128, 128, false), idO = tc::idesc_f16(128, D, true);
             int gc = 0, cnt0 = 0, cnt1 = 0, nq0 = 0, nq1 = 0;

@@ -6,6 +6,16 @@
 
 namespace xgr {
 
+// cp.async of 16 or 4 bytes, zeros where `in` is false (src is not read then)
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0)
+                 : "memory");
+}
+
 // the four codes of a word -> two fp16 pairs (elements 0, 1 and 2, 3)
 template <int FMT>
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {

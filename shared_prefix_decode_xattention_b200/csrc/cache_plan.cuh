@@ -71,14 +71,21 @@ struct Cursor {
     int units;       // its units
 };
 
+// Shared memory of plan_begin.
+template <int T>
+struct PlanSmem {
+    int64_t base[T / 32 + 1];
+    Cursor first;
+};
+
 // Every thread of the block gets the block's first cursor and [begin, end)
 // (false: no work).  T = threads of the block.
 template <int T>
-__device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_units,
+__device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_units, PlanSmem<T> &sm,
                                            const PlanOut &p, Cursor &cur, int64_t &begin, int64_t &end,
                                            int64_t &per) {
-    __shared__ int64_t base[T / 32 + 1];
-    __shared__ Cursor first;
+    int64_t *base = sm.base;
+    Cursor &first = sm.first;
     const int n_rows = a.c.n_rows;
     const int rpt = (n_rows + T - 1) / T;
     const int r0 = min((int)threadIdx.x * rpt, n_rows), r1 = min(r0 + rpt, n_rows);

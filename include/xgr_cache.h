@@ -116,7 +116,7 @@ typedef struct {
  * n_q_heads: a multiple of n_kv_heads.  Contents behind a row's length are
  * never used, whatever bits are there. */
 xgr_status xgr_cache_attend_bytes(const xgr_cache *cache, int32_t n_q_heads, int32_t n_rows,
-                                  size_t *bytes);
+                                  int32_t n_tokens, size_t *bytes);
 xgr_status xgr_cache_attend(const xgr_cache *cache, const xgr_cache_rows *rows, const int32_t *d_cu,
                             int32_t n_tokens, int32_t max_q, int32_t n_q_heads, const void *d_q,
                             int64_t q_stride, const xgr_attn_opts *opts, void *d_out, float *d_lse,

@@ -146,10 +146,10 @@ class PagedCache:
                                  None if slopes is None else slopes.data_ptr(),
                                  None if prefix is None else prefix.data_ptr(),
                                  None if first is None else first.data_ptr())
-        key = ("attend", hq, n_rows)
+        key = ("attend", hq, n_rows, n_tokens)
         need = self._need.get(key)
         if need is None:
-            need = self._need[key] = xgr.xgr_cache_attend_bytes(self._c, hq, n_rows)
+            need = self._need[key] = xgr.xgr_cache_attend_bytes(self._c, hq, n_rows, n_tokens)
         with self._guard():
             st = self._stream(stream)
             ws = self._workspace(fn, st, need)

@@ -62,6 +62,7 @@ struct AttendArgs {
     const int32_t *prefix;
     const int32_t *first;
     int whole;                  // 1: a work unit is a whole segment (every row is short)
+    int32_t *tile_lo;           // lowest visible key of each tile (with first)
     uint8_t *ws;
 };
 
@@ -94,7 +95,7 @@ struct StoreArgs {
     int max_n;
 };
 
-size_t attend_ws_bytes(int D, int n_rows);
+size_t attend_ws_bytes(int D, int G, int n_rows, int n_tokens);
 cudaError_t launch_cache_attend(const AttendArgs &a, cudaStream_t s);
 cudaError_t launch_cache_store(const StoreArgs &a, cudaStream_t s);
 cudaError_t launch_cache_fork(const ForkArgs &a, cudaStream_t s);

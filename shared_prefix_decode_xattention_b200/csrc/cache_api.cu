@@ -68,13 +68,13 @@ size_t words_of(const xgr_cache *c) { return ((size_t)c->n_pages + 31) / 32; }
 }  // namespace
 
 extern "C" xgr_status xgr_cache_attend_bytes(const xgr_cache *cache, int32_t n_q_heads, int32_t n_rows,
-                                             size_t *bytes) {
+                                             int32_t n_tokens, size_t *bytes) {
     int shift = 0;
     const xgr_status st = check_cache(cache, &shift);
     if (st != XGR_OK) return st;
     if (!bytes) return XGR_ERR_ARG;
-    if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads || n_rows < 0) return XGR_ERR_SHAPE;
-    *bytes = attend_ws_bytes(cache->head_dim, n_rows);
+    if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads || n_rows < 0 || n_tokens < 0) return XGR_ERR_SHAPE;
+    *bytes = attend_ws_bytes(cache->head_dim, n_q_heads / cache->n_kv_heads, n_rows, n_tokens);
     return XGR_OK;
 }
 
@@ -100,7 +100,7 @@ extern "C" xgr_status xgr_cache_attend(const xgr_cache *cache, const xgr_cache_r
     if (q_stride < (int64_t)n_q_heads * cache->head_dim || q_stride % 8) return XGR_ERR_SHAPE;
     if ((int64_t)n_tokens * n_q_heads > 0x7fffffffll || (int64_t)max_q * G > 0x3fffffffll) return XGR_ERR_SHAPE;
     if (!al(d_cu, 4) || !al(d_q, 16) || !al(d_out, 16) || !al(d_lse, 4) || !al(d_ws, kAlign)) return XGR_ERR_ARG;
-    if (ws_bytes < attend_ws_bytes(cache->head_dim, rows->n_rows)) return XGR_ERR_CAPACITY;
+    if (ws_bytes < attend_ws_bytes(cache->head_dim, G, rows->n_rows, n_tokens)) return XGR_ERR_CAPACITY;
     a.c.cu = d_cu;
     a.c.n_tokens = n_tokens;
     a.q = static_cast<const __nv_bfloat16 *>(d_q);

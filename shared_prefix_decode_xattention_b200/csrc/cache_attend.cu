@@ -93,10 +93,8 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
     for (int64_t at = begin; at < end;) {
         const RowSpan row = row_span(c, cur.r, a.max_q);
         const int u1 = (int)min((int64_t)cur.units, cur.u + (end - at));
-        const KeyRange tk = tile_keys(a, row, cur.r, R, cur.t);
-        const int unit0 = tk.lo / kUnitKeys;
-        int kb = a.whole ? tk.lo : max(tk.lo, (unit0 + cur.u) * kUnitKeys);
-        int ke = a.whole ? tk.hi : min(tk.hi, (unit0 + u1) * kUnitKeys);
+        const KeyRange sk = segment_keys(a, row, cur, u1, R);
+        int kb = sk.lo, ke = sk.hi;
 
         // ---- this lane's query rows: qr + 8 i of each 16-row tile
         int lo[2 * MT], hi[2 * MT], pos[2 * MT];
@@ -486,72 +484,98 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
     }
 }
 
-// A block per (token, query head): folds the partial results of a segment that
-// was cut.  O and l of part k count 2^(m_k - max m).
-template <int D>
-__global__ void __launch_bounds__(128) cache_join_kernel(AttendArgs a, int R, PlanOut po, int max_parts, float bias) {
-    extern __shared__ float wt[];   // [max_parts] weights
+// Folds the parts of the segments that were cut.  Column c of the grid looks at
+// the segment that CTA c begins in the middle of, and takes it if c is the first
+// such CTA; a row of the tile is folded by WPR warps (one where parts are few,
+// four, each every fourth part, where a long row may have many).  O and l of
+// part k count 2^(m_k - max m).
+template <int D, int WPR>
+__global__ void __launch_bounds__(128) cache_join_kernel(AttendArgs a, int R, PlanOut po, float bias) {
+    constexpr int N = D / 32;                       // dims of a lane
+    __shared__ float acc[4][D];
     __shared__ float red[4];
-    __shared__ float acc[2][D];
     griddep_wait();
     griddep_launch_dependents();
-    const CacheArgs &c = a.c;
-    const int tok = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-    int lo = 0, hi = c.n_rows - 1;
-    while (lo < hi) {   // the last row that begins at tok or before it
+    const Cursor cur = po.first[blockIdx.x];
+    if (cur.u == 0) return;
+    const int64_t per = *po.per;
+    const int64_t start = (int64_t)blockIdx.x * per - cur.u;     // the segment's first unit
+    const int c0 = (int)(start / per);
+    if (c0 != (int)blockIdx.x - 1) return;
+    const int n = (int)((start + cur.units - 1) / per) - c0 + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rr = blockIdx.y * (4 / WPR) + warp / WPR, sub = warp % WPR;
+    const RowSpan row = row_span(a.c, cur.r, a.max_q);
+    const int ia = cur.t * R + rr;
+    if (ia >= row.n * a.G) return;                  // (of all warps of a row)
+    auto part = [&](int k) { return ((int64_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * R + rr; };
+    float m = -INFINITY;
+    for (int k = lane; k < n; k += 32) m = fmaxf(m, po.ml[part(k)].x);
+    m = warp_max(m);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, x[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = 0.f;
+#pragma unroll 4
+    for (int k = sub; k < n; k += WPR) {
+        const int64_t pi = part(k);
+        const float2 ml = po.ml[pi];
+        const float f = exp2_fast(ml.x - ref);
+        l += f * ml.y;
+        if constexpr (N == 4) {
+            const float4 y = reinterpret_cast<const float4 *>(po.o + pi * D)[lane];
+            x[0] += f * y.x; x[1] += f * y.y; x[2] += f * y.z; x[3] += f * y.w;
+        } else {
+            const float2 y = reinterpret_cast<const float2 *>(po.o + pi * D)[lane];
+            x[0] += f * y.x; x[1] += f * y.y;
+        }
+    }
+    if constexpr (WPR > 1) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[warp][lane * N + e] = x[e];
+        if (lane == 0) red[warp] = l;
+        __syncthreads();
+        if (warp > 0) return;
+        l = red[0] + red[1] + red[2] + red[3];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int d = lane * N + e;
+            x[e] = acc[0][d] + acc[1][d] + acc[2][d] + acc[3][d];
+        }
+    }
+    const int64_t oi = (int64_t)(row.t0 + ia / a.G) * a.Hq + cur.g * a.G + ia % a.G;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(a.out + oi * D + lane * N);
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) dst[e] = __floats2bfloat162_rn(x[2 * e] * inv, x[2 * e + 1] * inv);
+    if (lane == 0) a.lse[oi] = l == 0.f ? -INFINITY : (ref - bias + log2f(l)) * kLn2;
+}
+
+// The lowest key that the queries of each tile see (the row's length where they
+// see none), a warp a tile: with documents in a row it may lie far above 0, and
+// the work has to be shared out without the keys below it.
+__global__ void __launch_bounds__(128) cache_tile_lo_kernel(AttendArgs a, int R, int64_t slots) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t slot = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+    if (slot >= slots) return;
+    int lo = 0, hi = a.c.n_rows - 1;
+    while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (c.cu[mid] <= tok) lo = mid;
+        if (tile_slot(a, mid, R) <= slot) lo = mid;
         else hi = mid - 1;
     }
-    const int r = lo;
-    const RowSpan row = row_span(c, r, a.max_q);
-    if (tok < row.t0 || tok >= row.t0 + row.n) return;
-    const int g = h / a.G, ia = (tok - row.t0) * a.G + h % a.G;
-    const int t = ia / R, rr = ia % R;
-    int64_t u = po.row_unit[r];
-    for (int i = 0; i < t; ++i) u += (int64_t)range_units(a, tile_keys(a, row, r, R, i)) * c.Hkv;
-    const int units = range_units(a, tile_keys(a, row, r, R, t));
-    u += (int64_t)g * units;
-    const int64_t per = *po.per;
-    const int c0 = (int)(u / per), c1 = (int)((u + units - 1) / per);
-    const int n = c1 - c0 + 1;
-    if (n == 1 || n > max_parts) return;   // (written whole)
-    auto part = [&](int k) { return ((int64_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * R + rr; };
-    const int tid = threadIdx.x, lane = tid % 32;
-    float m = -INFINITY;
-    for (int k = tid; k < n; k += 128) m = fmaxf(m, po.ml[part(k)].x);
-    m = warp_max(m);
-    if (lane == 0) red[tid / 32] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    __syncthreads();
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int k = tid; k < n; k += 128) {
-        const float2 ml = po.ml[part(k)];
-        const float f = exp2_fast(ml.x - ref);
-        wt[k] = f;
-        l += f * ml.y;
+    const RowSpan row = row_span(a.c, lo, a.max_q);
+    const int64_t t = slot - tile_slot(a, lo, R);
+    if (t < 0 || t >= row_tiles(a, row, R)) return;
+    const int i0 = (int)(t * R / a.G), i1 = (int)((min((t + 1) * R, (int64_t)row.n * a.G) - 1) / a.G);
+    int low = row.len;
+    for (int i = i0 + (int)(threadIdx.x % 32); i <= i1; i += 32) {
+        const KeyRange q = query_keys(a, row, lo, i);
+        if (q.lo < q.hi) low = min(low, q.lo);
     }
-    l = warp_sum(l);
-    if (lane == 0) red[tid / 32] = l;
-    __syncthreads();
-    l = red[0] + red[1] + red[2] + red[3];
-    const int d = tid % D, half = tid / D;           // D = 64: two threads a dim
-    constexpr int kSplit = 128 / D;
-    float x = 0.f;
-#pragma unroll 8
-    for (int k = half; k < n; k += kSplit) x += wt[k] * po.o[part(k) * D + d];
-    if constexpr (kSplit == 2) {
-        acc[half][d] = x;
-        __syncthreads();
-        x = acc[0][d] + acc[1][d];
-    }
-    if (half == 0) {
-        const int64_t oi = (int64_t)tok * a.Hq + h;
-        a.out[oi * D + d] = __float2bfloat16(l == 0.f ? 0.f : x / l);
-        if (d == 0) a.lse[oi] = l == 0.f ? -INFINITY : (ref - bias + log2f(l)) * kLn2;
-    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (threadIdx.x % 32 == 0) a.tile_lo[slot] = low;
 }
 
 constexpr int kSmallCtas = 3 * kSms;         // 16-row tiles: three CTAs an SM
@@ -563,16 +587,17 @@ constexpr int kWholeUnits = 8;               // rows of at most this many units 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct WsLayout {
-    size_t rows, per, o, ml, total;
+    size_t first, per, o, ml, lo, total;
 };
-WsLayout ws_layout(int D, int n_rows) {
+WsLayout ws_layout(int D, int G, int n_rows, int n_tokens) {
     WsLayout w{};
-    w.rows = 0;
-    w.per = up256((size_t)n_rows * 8);
+    w.first = 0;
+    w.per = up256((size_t)kSmallCtas * sizeof(Cursor));
     w.o = w.per + 256;
     const size_t parts = 2 * std::max<size_t>({(size_t)kSmallCtas * 16, (size_t)kWideCtas * 32, (size_t)kSms * kTcRows256});
     w.ml = w.o + up256(parts * D * 4);
-    w.total = w.ml + up256(parts * 8);
+    w.lo = w.ml + up256(parts * 8);
+    w.total = w.lo + up256((size_t)((int64_t)n_tokens * G / 16 + n_rows) * 4);   // (16: the lowest tile)
     return w;
 }
 
@@ -601,7 +626,7 @@ cudaError_t launch_kind(const AttendArgs &a, int R, const PlanOut &po, int ctas,
 
 }  // namespace
 
-size_t attend_ws_bytes(int D, int n_rows) { return ws_layout(D, n_rows).total; }
+size_t attend_ws_bytes(int D, int G, int n_rows, int n_tokens) { return ws_layout(D, G, n_rows, n_tokens).total; }
 
 cudaError_t launch_cache_attend(const AttendArgs &in, cudaStream_t s) {
     AttendArgs a = in;
@@ -616,15 +641,21 @@ cudaError_t launch_cache_attend(const AttendArgs &in, cudaStream_t s) {
     const int64_t segs = (((int64_t)c.n_tokens * a.G + R - 1) / R + c.n_rows) * c.Hkv;
     const int64_t row_units = a.whole ? 1 : (int64_t)c.max_pages * c.page / kUnitKeys + 2;
     const int ctas = (int)std::min<int64_t>(cap, (segs * row_units + min_units - 1) / min_units);
+    const WsLayout l = ws_layout(c.D, a.G, c.n_rows, c.n_tokens);
+    a.tile_lo = reinterpret_cast<int32_t *>(a.ws + l.lo);
     PlanOut po{};
     if (!a.whole) {
-        const WsLayout l = ws_layout(c.D, c.n_rows);
-        po.row_unit = reinterpret_cast<int64_t *>(a.ws + l.rows);
+        po.first = reinterpret_cast<Cursor *>(a.ws + l.first);
         po.per = reinterpret_cast<int64_t *>(a.ws + l.per);
         po.o = reinterpret_cast<float *>(a.ws + l.o);
         po.ml = reinterpret_cast<float2 *>(a.ws + l.ml);
     }
     cudaError_t e;
+    if (a.first) {
+        const int64_t slots = (int64_t)c.n_tokens * a.G / R + c.n_rows;
+        e = launch_pdl(cache_tile_lo_kernel, dim3((unsigned)((slots + 3) / 4)), dim3(128), 0, s, a, R, slots);
+        if (e != cudaSuccess) return e;
+    }
     if (c.D == 128)
         e = c.fmt == XGR_CACHE_E4M3 ? launch_kind<128, XGR_CACHE_E4M3>(a, R, po, ctas, min_units, s)
                                     : launch_kind<128, XGR_CACHE_INT8>(a, R, po, ctas, min_units, s);
@@ -632,10 +663,15 @@ cudaError_t launch_cache_attend(const AttendArgs &in, cudaStream_t s) {
         e = c.fmt == XGR_CACHE_E4M3 ? launch_kind<64, XGR_CACHE_E4M3>(a, R, po, ctas, min_units, s)
                                     : launch_kind<64, XGR_CACHE_INT8>(a, R, po, ctas, min_units, s);
     if (e != cudaSuccess || a.whole) return e;
-    const dim3 grid((unsigned)((int64_t)c.n_tokens * a.Hq));
     const float bias = R == kTcRows256 ? kTcBias : kBias;
-    return c.D == 128 ? launch_pdl(cache_join_kernel<128>, grid, dim3(128), (size_t)ctas * 4, s, a, R, po, ctas, bias)
-                      : launch_pdl(cache_join_kernel<64>, grid, dim3(128), (size_t)ctas * 4, s, a, R, po, ctas, bias);
+    if (R == kTcRows256) {
+        const dim3 grid(ctas, R / 4);
+        return c.D == 128 ? launch_pdl(cache_join_kernel<128, 1>, grid, dim3(128), 0, s, a, R, po, bias)
+                          : launch_pdl(cache_join_kernel<64, 1>, grid, dim3(128), 0, s, a, R, po, bias);
+    }
+    const dim3 grid(ctas, R);
+    return c.D == 128 ? launch_pdl(cache_join_kernel<128, 4>, grid, dim3(128), 0, s, a, R, po, bias)
+                      : launch_pdl(cache_join_kernel<64, 4>, grid, dim3(128), 0, s, a, R, po, bias);
 }
 
 }  // namespace xgr

@@ -169,31 +169,38 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             const int n = s.tile_chunks(h);
             const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
             const int pos = s.row.len - s.row.n + tok;
-            // ---- the query row as fp16, near 1
+            // ---- the warp's 32 query rows as fp16, near 1: D / 8 lanes a row, so that loads are whole lines
             float fac = 0.f;
             if (n > 0 || (s.narrow && s.chunks > 0)) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (int64_t)(s.row.t0 + tok) * a.q_stride +
-                                                                   (int64_t)head * D);
-                float top = 0.f;
+                constexpr int kPer = 256 / D;          // rows of one load of the warp
+                const int64_t q_off = valid ? (int64_t)(s.row.t0 + tok) * a.q_stride + (int64_t)head * D : -1;
+                const int ln = lane % (D / 8);
+                uint4 v[32 / kPer];                    // all loads in flight at once
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    float f[8];
-                    unpack8(valid ? src[i] : make_uint4(0, 0, 0, 0), f);
+                for (int i = 0; i < 32 / kPer; ++i) {
+                    const int64_t off = __shfl_sync(0xffffffffu, q_off, i * kPer + lane / (D / 8));
+                    v[i] = off >= 0 ? *reinterpret_cast<const uint4 *>(a.q + off + 8 * ln) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 32 / kPer; ++i) {
+                    float f[8], top = 0.f;
+                    unpack8(v[i], f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-                }
-                const int ex = query_exp(top);
-                fac = a.scale * pow2i(ex);
-                if (!s.narrow || h == 0) {
-                    const float down = pow2i(-ex);
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        float f[8];
-                        unpack8(valid ? src[i] : make_uint4(0, 0, 0, 0), f);
-                        *reinterpret_cast<uint4 *>(base + L::q + h * L::kTile + sw128<D>(tr, i)) =
+                    for (int o = 1; o < D / 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int ex = query_exp(top);
+                    const float mine = __shfl_sync(0xffffffffu, a.scale * pow2i(ex), (lane % kPer) * (D / 8));
+                    if (lane / kPer == i) fac = mine;
+                    if (!s.narrow || h == 0) {
+                        const float down = pow2i(-ex);
+                        const int rr = 32 * (warp & 3) + i * kPer + lane / (D / 8);
+                        *reinterpret_cast<uint4 *>(base + L::q + h * L::kTile + sw128<D>(rr, ln)) =
                             make_uint4(pack_f16(f[0] * down, f[1] * down), pack_f16(f[2] * down, f[3] * down),
                                        pack_f16(f[4] * down, f[5] * down), pack_f16(f[6] * down, f[7] * down));
                     }
+                }
+                if (!s.narrow || h == 0) {
                     fence_async_smem();
                     mbar_arrive(bar(B_QFULL + h));
                 }
@@ -334,10 +341,24 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 const int64_t pi = ((int64_t)blockIdx.x * 2 + (cur.u == 0 ? 1 : 0)) * R + tr + 128 * h;
                 const float ref = M == -INFINITY ? 0.f : M;
                 const float scale = !all ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                // rows go out through the warp's share of the Q tile (no product reads it any more), 2 D bytes a
+                // row at a time, so that stores are whole lines
+                uint8_t *stage = base + L::q + h * L::kTile + (warp & 3) * (L::kTile / 4);
+                auto slot = [&](int row, int ch) { return stage + row * (2 * D) + ((ch ^ (row & 7)) << 4); };
+                auto flush = [&](uint8_t *dst, int64_t row_bytes, int64_t my_row) {   // lane's row of the result (-1: none)
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = 0; i < D / 8; ++i) {
+                        const int rr = i * (256 / D) + lane / (D / 8), ch = lane % (D / 8);
+                        const int64_t row = __shfl_sync(0xffffffffu, my_row, rr);
+                        const uint4 y = *reinterpret_cast<const uint4 *>(slot(rr, ch));
+                        if (row >= 0) reinterpret_cast<uint4 *>(dst + row * row_bytes)[ch] = y;
+                    }
+                    __syncwarp();
+                };
 #pragma unroll 1
                 for (int p = 0; p < D / 32; ++p) {
                     float o[32];
-                    __syncwarp();
                     if (n > 0) {
                         tc::ld32(to + 32u * p, o);
                         tc::wait_ld_into(o);
@@ -352,8 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = o[e] * a0 + o1[e] * a1;
                     }
-                    if (valid && all) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + oi * D + 32 * p);
+                    if (all) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint4 pk;
@@ -361,15 +381,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 b[j] = __floats2bfloat162_rn(o[8 * e + 2 * j] * scale, o[8 * e + 2 * j + 1] * scale);
-                            dst[e] = pk;
+                            *reinterpret_cast<uint4 *>(slot(lane, 4 * p + e)) = pk;
                         }
-                    } else if (valid) {
-                        float4 *dst = reinterpret_cast<float4 *>(po.o + pi * D + 32 * p);
+                    } else {
+                        constexpr int kHalves = D / 64;   // 32-dim pieces of a pass of fp32
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                            *reinterpret_cast<float4 *>(slot(lane, 8 * (p % kHalves) + e)) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        if (p % kHalves == kHalves - 1)
+                            flush(reinterpret_cast<uint8_t *>(po.o) + (p / kHalves) * (2 * D), 4 * D, valid ? pi : -1);
                     }
                 }
+                if (all) flush(reinterpret_cast<uint8_t *>(a.out), 2 * D, valid ? oi : -1);
                 if (valid) {
                     if (all) a.lse[oi] = l == 0.f ? -INFINITY : (ref - kTcBias + log2f(l)) * kLn2;
                     else po.ml[pi] = make_float2(M, l);

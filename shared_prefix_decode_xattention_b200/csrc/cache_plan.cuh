@@ -8,9 +8,10 @@
 // CTAs evenly, however few they are.  A segment cut by a CTA's end leaves
 // partial results (O relative to its reference, m, l) in the workspace, at most
 // two a CTA (the segment it continues, slot 0, and the one it leaves
-// unfinished, slot 1), and the join kernel folds them.  Lengths are read on the
-// device, so nothing waits for the host; every CTA works the plan out anew
-// from d_cu and d_len, and the first one leaves it for the join.
+// unfinished, slot 1), and the join kernel folds them: every cut segment is the
+// one that some CTA begins in the middle of, so it runs over the CTAs' first
+// cursors.  Lengths are read on the device, so nothing waits for the host;
+// every CTA works the plan out anew from d_cu and d_len.
 //
 // In "whole" mode (every row is short) a unit is a whole segment: nothing is
 // cut and no join runs.
@@ -22,19 +23,33 @@ namespace xgr {
 
 constexpr int kUnitKeys = 128;
 
-// Results of a segment or of a part of it are joined from these.
+// Where a CTA stands in the line.
+struct Cursor {
+    int r, t, g;     // segment
+    int u;           // unit within it
+    int units;       // its units
+};
+
+// Results of parts of segments, for the join (null in whole mode).
 struct PlanOut {
-    int64_t *row_unit;   // [n_rows] first unit of each row
+    Cursor *first;       // [N] each CTA's first cursor (u = 0: it cuts nothing)
     int64_t *per;        // [1] units a CTA takes
     float *o;            // [N][2][R][D]
     float2 *ml;          // [N][2][R]
 };
 
-// The keys [lo, hi) that some query of tile t may see, by position alone
-// (d_first can only narrow it), of a row with span s.
 struct KeyRange {
     int lo, hi;
 };
+
+// Where d_first is given, the lowest key that a tile's queries see is worked out
+// by a kernel of its own first, into one slot a tile: row r's tiles begin at
+// tile_slot (no row has more tiles than the gap to the next row's slots).
+__device__ __forceinline__ int64_t tile_slot(const AttendArgs &a, int r, int R) {
+    return (int64_t)a.c.cu[r] * a.G / R + r;
+}
+
+// The keys [lo, hi) that some query of tile t of a row with span s may see.
 
 __device__ __forceinline__ KeyRange tile_keys(const AttendArgs &a, const RowSpan &s, int r, int R, int t) {
     KeyRange k{0, s.len};
@@ -45,6 +60,7 @@ __device__ __forceinline__ KeyRange tile_keys(const AttendArgs &a, const RowSpan
         if (a.prefix) k.hi = max(k.hi, min(a.prefix[r], s.len));
     }
     if (a.window > 0) k.lo = max(0, p0 + i0 - a.window + 1);
+    if (a.first) k.lo = max(k.lo, a.tile_lo[tile_slot(a, r, R) + t]);
     return k;
 }
 
@@ -63,13 +79,6 @@ __device__ __forceinline__ int64_t row_units(const AttendArgs &a, const RowSpan 
     for (int t = 0; t < tiles; ++t) u += range_units(a, tile_keys(a, s, r, R, t));
     return u * a.c.Hkv;
 }
-
-// Where a CTA stands in the line.
-struct Cursor {
-    int r, t, g;     // segment
-    int u;           // unit within it
-    int units;       // its units
-};
 
 // Shared memory of plan_begin.
 template <int T>
@@ -109,15 +118,11 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_u
     per = max((int64_t)min_units, (total + gridDim.x - 1) / gridDim.x);
     begin = blockIdx.x * per;
     end = min(begin + per, total);
-    if (blockIdx.x == 0 && p.row_unit) {
-        int64_t at = from;
-        for (int r = r0; r < r1; ++r) {
-            p.row_unit[r] = at;
-            at += row_units(a, row_span(a.c, r, a.max_q), r, R);
-        }
-        if (threadIdx.x == 0) *p.per = per;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.per) *p.per = per;
+    if (begin >= end) {
+        if (threadIdx.x == 0 && p.first) p.first[blockIdx.x] = Cursor{0, 0, 0, 0, 0};
+        return false;
     }
-    if (begin >= end) return false;
     if (from <= begin && begin < from + mine) {
         int64_t left = begin - from;
         int r = r0;
@@ -139,6 +144,7 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_u
         first.g = (int)(left / units);
         first.u = (int)(left % units);
         first.units = units;
+        if (p.first) p.first[blockIdx.x] = first;
     }
     __syncthreads();
     cur = first;
@@ -172,25 +178,13 @@ __device__ __forceinline__ KeyRange query_keys(const AttendArgs &a, const RowSpa
     return k;
 }
 
-// The keys [kb, ke) of units [cur.u, u1) of segment cur that some query of its
-// tile sees (empty: none), worked out by a whole warp.
+// The keys of units [cur.u, u1) of segment cur (hi <= lo: none).
 __device__ __forceinline__ KeyRange segment_keys(const AttendArgs &a, const RowSpan &s, const Cursor &cur, int u1,
                                                  int R) {
-    KeyRange k = tile_keys(a, s, cur.r, R, cur.t);
-    if (!a.whole) {
-        const int unit0 = k.lo / kUnitKeys;
-        k = KeyRange{max(k.lo, (unit0 + cur.u) * kUnitKeys), min(k.hi, (unit0 + u1) * kUnitKeys)};
-    }
-    if (a.first) {
-        const int i0 = cur.t * R / a.G, i1 = (min((cur.t + 1) * R, s.n * a.G) - 1) / a.G;
-        int lo = 0x7fffffff;
-        for (int i = i0 + (int)(threadIdx.x % 32); i <= i1; i += 32) {
-            const KeyRange q = query_keys(a, s, cur.r, i);
-            if (q.lo < q.hi) lo = min(lo, q.lo);
-        }
-        k.lo = max(k.lo, __reduce_min_sync(0xffffffffu, lo));
-    }
-    return k;
+    const KeyRange k = tile_keys(a, s, cur.r, R, cur.t);
+    if (a.whole) return k;
+    const int unit0 = k.lo / kUnitKeys;
+    return KeyRange{max(k.lo, (unit0 + cur.u) * kUnitKeys), min(k.hi, (unit0 + u1) * kUnitKeys)};
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {   // one MUFU op; tiny results flush to 0

@@ -188,7 +188,7 @@ def lib():
         "xgr_decode_graph_kernels": [P, ctypes.POINTER(i32)],
         "xgr_decode_graph_destroy": [P],
         # the paged 8-bit KV cache (include/xgr_cache.h)
-        "xgr_cache_attend_bytes": [PC, i32, i32, PZ],
+        "xgr_cache_attend_bytes": [PC, i32, i32, i32, PZ],
         "xgr_cache_attend": [PC, PR, P, i32, i32, i32, P, i64, ctypes.POINTER(xgr_attn_opts), P, P, P,
                              ctypes.c_size_t, P, P],
         "xgr_cache_store": [PC, PR, P, i32, i32, P, P, i64, P, P],
@@ -398,10 +398,11 @@ def xgr_decode_graph_destroy(graph: int) -> None:
 
 # ---- the paged 8-bit KV cache (include/xgr_cache.h; cache.PagedCache wraps these)
 
-def xgr_cache_attend_bytes(cache: xgr_cache, n_q_heads: int, n_rows: int) -> int:
+def xgr_cache_attend_bytes(cache: xgr_cache, n_q_heads: int, n_rows: int, n_tokens: int) -> int:
     n = ctypes.c_size_t(0)
     _check("xgr_cache_attend_bytes",
-           lib().xgr_cache_attend_bytes(ctypes.byref(cache), n_q_heads, n_rows, ctypes.byref(n)))
+           lib().xgr_cache_attend_bytes(ctypes.byref(cache), n_q_heads, n_rows, n_tokens,
+                                        ctypes.byref(n)))
     return n.value
 
 

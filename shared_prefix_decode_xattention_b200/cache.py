@@ -16,9 +16,6 @@ the capture, on the capturing stream.
 """
 from __future__ import annotations
 
-import ctypes
-from typing import Optional
-
 from . import xgr
 
 _MASKS = {"full": xgr.XGR_ATTN_FULL, "causal": xgr.XGR_ATTN_CAUSAL, "prefix": xgr.XGR_ATTN_CAUSAL}
@@ -45,14 +42,16 @@ class PagedCache:
             if not t.is_cuda or t.device != k.device or not t.is_contiguous():
                 _bad("PagedCache", "tensors: contiguous, on one CUDA device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device = k.device
+        self.device, self._index = k.device, k.get_device()
+        self._i32, self._bf16, self._f32 = torch.int32, torch.bfloat16, torch.float32
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self._c = xgr.xgr_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                 self.n_pages, self.page_size, self.n_kv_heads, self.head_dim,
                                 fmt[k.dtype])
         xgr.xgr_cache_compact_bytes(self._c)      # refuses shapes the library does not take
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self._ws = {}                             # stream handle -> its workspace
+        self._d_status = self._status.data_ptr()
+        self._ws = {}                             # stream handle -> its workspace (tensor, bytes, address)
         self._old = []                            # outgrown workspaces: a captured graph may use them
         self._need = {}                           # (call, sizes) -> bytes
 
@@ -68,51 +67,68 @@ class PagedCache:
         return cls(*codes, *scales)
 
     # ------------------------------------------------------------------ checks
-    def _i32(self, fn, name, t, shape):
-        if t.dtype != self._torch.int32 or t.device != self.device or tuple(t.shape) != shape \
-                or not t.is_contiguous():
+    def _int32(self, fn, name, t, shape):
+        if t.dtype is not self._i32 or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
             _bad(fn, f"{name}: contiguous int32 {list(shape)} on {self.device}")
+        return t.data_ptr()
 
     def _rows(self, fn, table, length):
         if table.dim() != 2:
             _bad(fn, "table: int32 [n_rows][max_pages]")
         n_rows, width = table.shape
-        self._i32(fn, "table", table, (n_rows, width))
-        self._i32(fn, "length", length, (n_rows,))
-        return xgr.xgr_cache_rows(n_rows, width, table.data_ptr(), length.data_ptr())
+        return xgr.xgr_cache_rows(n_rows, width, self._int32(fn, "table", table, table.shape),
+                                  self._int32(fn, "length", length, (n_rows,)))
 
     def _tokens(self, fn, name, t, heads):
         """Packed tokens [n][heads][D] bf16, each token's heads contiguous; the token stride."""
-        if t.dim() != 3 or t.dtype != self._torch.bfloat16 or t.device != self.device \
-                or t.shape[2] != self.head_dim or (heads is not None and t.shape[1] != heads):
-            _bad(fn, f"{name}: bf16 [n_tokens][{heads or 'heads'}][{self.head_dim}] on {self.device}")
-        line = t.shape[1] * t.shape[2]
-        stride = t.stride(0) if t.shape[0] > 1 else line
-        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]) or stride < line:
+        if t.dim() != 3 or t.dtype is not self._bf16 or t.get_device() != self._index:
+            _bad(fn, f"{name}: bf16 [n_tokens][heads][{self.head_dim}] on {self.device}")
+        n, h, d = t.shape
+        if d != self.head_dim or (heads is not None and h != heads):
+            _bad(fn, f"{name}: bf16 [n_tokens][{heads or 'heads'}][{self.head_dim}]")
+        if t.is_contiguous():
+            return h * d
+        stride, across, along = t.stride()
+        if n <= 1:
+            stride = max(stride, h * d)
+        if along != 1 or (h > 1 and across != d) or stride < h * d:
             _bad(fn, f"{name}: the heads of a token contiguous", xgr.XGR_ERR_SHAPE)
         return stride
 
     def _stream(self, stream):
         if stream is None:
-            return self._torch.cuda.current_stream(self.device).cuda_stream
+            return self._torch.cuda.current_stream(self._index).cuda_stream
         return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _bytes(self, key, size):
+        need = self._need.get(key)
+        if need is None:
+            if len(self._need) >= 256:
+                self._need.clear()
+            need = self._need[key] = size()
+        return need
 
     def _workspace(self, fn, stream, need):
         ws = self._ws.get(stream)
-        if ws is None or ws.numel() < need:
+        if ws is None or ws[1] < need:
             torch = self._torch
             if torch.cuda.is_current_stream_capturing():
                 _bad(fn, "no workspace of this size on the capturing stream yet: make the call once "
                          "before the capture", xgr.XGR_ERR_STATE)
             if ws is not None:
-                self._old.append(ws)
-                need = max(need, 2 * ws.numel())
-            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            self._ws[stream] = ws
+                self._old.append(ws[0])
+                need = max(need, 2 * ws[1])
+            t = torch.empty(need, dtype=torch.uint8, device=self.device)
+            ws = self._ws[stream] = (t, need, t.data_ptr())
         return ws
 
-    def _guard(self):
-        return self._torch.cuda.device(self.device)
+    def _run(self, call, *args):
+        """The C call on the cache's device (a context's current device is the thread's)."""
+        cuda = self._torch.cuda
+        if cuda.current_device() == self._index:
+            return call(*args)
+        with cuda.device(self._index):
+            return call(*args)
 
     # ------------------------------------------------------------------ calls
     def attend(self, table, length, cu, q, out, lse, *, max_q: int, scale: float = 0.0, softcap: float = 0.0,
@@ -121,89 +137,91 @@ class PagedCache:
         [T][Hq][D] (bf16) and lse [T][Hq] (fp32); cu int32 [n_rows + 1].  mask: "full", "causal",
         or "prefix" (causal beside a bidirectional prefix of prefix[r] tokens).  See
         xgr_cache_attend."""
-        fn, torch = "PagedCache.attend", self._torch
+        self._run(self._attend, table, length, cu, q, out, lse, max_q, scale, softcap, mask, window, slopes,
+                  prefix, first, stream)
+
+    def _attend(self, table, length, cu, q, out, lse, max_q, scale, softcap, mask, window, slopes, prefix,
+                first, stream):
+        fn, index = "PagedCache.attend", self._index
         rows = self._rows(fn, table, length)
         n_rows = rows.n_rows
         if mask not in _MASKS or (mask == "prefix") != (prefix is not None):
             _bad(fn, "mask: 'full', 'causal', or 'prefix' with prefix int32 [n_rows]")
         stride = self._tokens(fn, "q", q, None)
-        n_tokens, hq = q.shape[0], q.shape[1]
-        self._i32(fn, "cu", cu, (n_rows + 1,))
-        if out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous() \
-                or out.device != self.device:
+        n_tokens, hq, _ = q.shape
+        d_cu = self._int32(fn, "cu", cu, (n_rows + 1,))
+        if out.dtype is not self._bf16 or out.shape != q.shape or not out.is_contiguous() \
+                or out.get_device() != index:
             _bad(fn, "out: contiguous bf16 of q's shape")
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (n_tokens, hq) or not lse.is_contiguous() \
-                or lse.device != self.device:
+        if lse.dtype is not self._f32 or lse.shape != (n_tokens, hq) or not lse.is_contiguous() \
+                or lse.get_device() != index:
             _bad(fn, "lse: contiguous fp32 [n_tokens][Hq]")
-        if slopes is not None and (slopes.dtype != torch.float32 or tuple(slopes.shape) != (hq,)
-                                   or not slopes.is_contiguous() or slopes.device != self.device):
-            _bad(fn, "slopes: contiguous fp32 [Hq]")
+        opts = xgr.xgr_attn_opts(scale, softcap, _MASKS[mask], window)
+        if slopes is not None:
+            if slopes.dtype is not self._f32 or slopes.shape != (hq,) or not slopes.is_contiguous() \
+                    or slopes.get_device() != index:
+                _bad(fn, "slopes: contiguous fp32 [Hq]")
+            opts.d_slopes = slopes.data_ptr()
         if prefix is not None:
-            self._i32(fn, "prefix", prefix, (n_rows,))
+            opts.d_prefix = self._int32(fn, "prefix", prefix, (n_rows,))
         if first is not None:
-            self._i32(fn, "first", first, (n_tokens,))
-        opts = xgr.xgr_attn_opts(scale, softcap, _MASKS[mask], window,
-                                 None if slopes is None else slopes.data_ptr(),
-                                 None if prefix is None else prefix.data_ptr(),
-                                 None if first is None else first.data_ptr())
-        key = ("attend", hq, n_rows, n_tokens)
-        need = self._need.get(key)
-        if need is None:
-            need = self._need[key] = xgr.xgr_cache_attend_bytes(self._c, hq, n_rows, n_tokens)
-        with self._guard():
-            st = self._stream(stream)
-            ws = self._workspace(fn, st, need)
-            xgr.xgr_cache_attend(self._c, rows, cu, n_tokens, max_q, hq, q, stride, opts, out, lse, ws,
-                                 ws.numel(), self._status, st)
+            opts.d_first = self._int32(fn, "first", first, (n_tokens,))
+        need = self._bytes(("attend", hq, n_rows, n_tokens),
+                           lambda: xgr.xgr_cache_attend_bytes(self._c, hq, n_rows, n_tokens))
+        st = self._stream(stream)
+        _, size, d_ws = self._workspace(fn, st, need)
+        xgr.xgr_cache_attend(self._c, rows, d_cu, n_tokens, max_q, hq, q.data_ptr(), stride, opts,
+                             out.data_ptr(), lse.data_ptr(), d_ws, size, self._d_status, st)
 
     def store(self, table, length, cu, k, v, *, max_n: int, stream=None):
         """Quantises the rows' new tokens k, v [T][Hkv][D] (bf16) into their pages; length counts
         them already.  See xgr_cache_store."""
+        self._run(self._store, table, length, cu, k, v, max_n, stream)
+
+    def _store(self, table, length, cu, k, v, max_n, stream):
         fn = "PagedCache.store"
         rows = self._rows(fn, table, length)
         stride = self._tokens(fn, "k", k, self.n_kv_heads)
         if v.shape != k.shape or self._tokens(fn, "v", v, self.n_kv_heads) != stride:
             _bad(fn, "k, v: the same shape and token stride", xgr.XGR_ERR_SHAPE)
-        self._i32(fn, "cu", cu, (rows.n_rows + 1,))
-        with self._guard():
-            xgr.xgr_cache_store(self._c, rows, cu, k.shape[0], max_n, k, v, stride, self._status,
-                                self._stream(stream))
+        d_cu = self._int32(fn, "cu", cu, (rows.n_rows + 1,))
+        xgr.xgr_cache_store(self._c, rows, d_cu, k.shape[0], max_n, k.data_ptr(), v.data_ptr(), stride,
+                            self._d_status, self._stream(stream))
 
     def fork(self, table, length, parent, n_new, table_out, len_out, *, stream=None):
         """The rows of the next step from their parents (-1: none), with pages for n_new[r] more
         tokens (None: none).  See xgr_cache_fork."""
+        self._run(self._fork, table, length, parent, n_new, table_out, len_out, stream)
+
+    def _fork(self, table, length, parent, n_new, table_out, len_out, stream):
         fn = "PagedCache.fork"
         rows = self._rows(fn, table, length)
-        n_out = parent.shape[0] if parent.dim() == 1 else -1
-        self._i32(fn, "parent", parent, (n_out,))
-        if n_new is not None:
-            self._i32(fn, "n_new", n_new, (n_out,))
-        self._i32(fn, "table_out", table_out, (n_out, rows.max_pages))
-        self._i32(fn, "len_out", len_out, (n_out,))
-        key = ("fork", n_out)
-        need = self._need.get(key)
-        if need is None:
-            need = self._need[key] = xgr.xgr_cache_fork_bytes(self._c, n_out)
-        with self._guard():
-            st = self._stream(stream)
-            ws = self._workspace(fn, st, need)
-            xgr.xgr_cache_fork(self._c, rows, n_out, parent, n_new, table_out, len_out, ws, ws.numel(),
-                               self._status, st)
+        if parent.dim() != 1:
+            _bad(fn, "parent: int32 [n_out]")
+        n_out = parent.shape[0]
+        d_parent = self._int32(fn, "parent", parent, (n_out,))
+        d_new = None if n_new is None else self._int32(fn, "n_new", n_new, (n_out,))
+        d_table = self._int32(fn, "table_out", table_out, (n_out, rows.max_pages))
+        d_len = self._int32(fn, "len_out", len_out, (n_out,))
+        need = self._bytes(("fork", n_out), lambda: xgr.xgr_cache_fork_bytes(self._c, n_out))
+        st = self._stream(stream)
+        _, size, d_ws = self._workspace(fn, st, need)
+        xgr.xgr_cache_fork(self._c, rows, n_out, d_parent, d_new, d_table, d_len, d_ws, size, self._d_status, st)
 
     def compact(self, table, length, table_out, n_used, *, stream=None):
         """Moves the pages that the rows hold to the front; n_used int32 [1].  See
         xgr_cache_compact."""
+        self._run(self._compact, table, length, table_out, n_used, stream)
+
+    def _compact(self, table, length, table_out, n_used, stream):
         fn = "PagedCache.compact"
         rows = self._rows(fn, table, length)
-        self._i32(fn, "table_out", table_out, tuple(table.shape))
-        self._i32(fn, "n_used", n_used, (1,))
-        need = self._need.get("compact")
-        if need is None:
-            need = self._need["compact"] = xgr.xgr_cache_compact_bytes(self._c)
-        with self._guard():
-            st = self._stream(stream)
-            ws = self._workspace(fn, st, need)
-            xgr.xgr_cache_compact(self._c, rows, table_out, n_used, ws, ws.numel(), self._status, st)
+        d_table = self._int32(fn, "table_out", table_out, table.shape)
+        d_used = self._int32(fn, "n_used", n_used, (1,))
+        need = self._bytes("compact", lambda: xgr.xgr_cache_compact_bytes(self._c))
+        st = self._stream(stream)
+        _, size, d_ws = self._workspace(fn, st, need)
+        xgr.xgr_cache_compact(self._c, rows, d_table, d_used, d_ws, size, self._d_status, st)
 
     def device_status(self) -> int:
         """Waits for the cache's device, returns the status word's bits (XGR_DEV_*) and clears them."""

@@ -167,6 +167,10 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
         const int mine = (tiles - warp + kWarps - 1) / kWarps;   // of this warp (tiles >= 0, warp < kWarps)
         const int32_t *line = c.table + (int64_t)cur.r * c.max_pages;
 
+        const int64_t page_bytes = (int64_t)c.Hkv * c.page * D, head_off = (int64_t)cur.g * c.page * D;
+        // this lane's place in 512 copied bytes (32 / kChunks keys), swizzled
+        const int kl0 = lane / kChunks;
+        const uint32_t lane_dst = kl0 * D + ((lane % kChunks ^ swz<D>(kl0)) << 4);
         // pages of the two halves of the warp's i-th tile (-2: no keys there, -1: no such page)
         auto ids_of = [&](int i, int *id) {
 #pragma unroll
@@ -182,22 +186,27 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
                 }
             }
         };
+        // Copies the warp's i-th tile: 16 keys of a page and head are contiguous, so a half is a base and offsets
+        // that do not depend on the tile.
         auto issue = [&](int i, const int *id) {
             if (i < mine) {
                 const int st = i % kStages;
                 const int key0 = kb0 + (warp + kWarps * i) * kTileKeys;
-                const uint32_t dst = ring0 + st * Smem<D, MT>::kStageBytes;
+                const uint32_t dst = ring0 + st * Smem<D, MT>::kStageBytes + lane_dst;
 #pragma unroll
-                for (int n = 0; n < kChunks; ++n) {          // 32 keys x kChunks chunks over 32 lanes
-                    const int idx = n * 32 + lane;
-                    const int kl = idx / kChunks, ch = idx % kChunks;
-                    const int page = kl < 16 ? id[0] : id[1];
-                    const bool in = page >= 0 && key0 + kl < ke;
-                    const int64_t off = in ? (((int64_t)page * c.Hkv + cur.g) * c.page + ((key0 + kl) & (c.page - 1))) * D + ch * 16
-                                           : 0;
-                    const uint32_t to = dst + kl * D + ((ch ^ swz<D>(kl)) << 4);
-                    cp_async16_zfill(to, c.k + off, in);
-                    cp_async16_zfill(to + kTileKeys * D, c.v + off, in);
+                for (int h = 0; h < 2; ++h) {
+                    const int left = id[h] >= 0 ? ke - key0 - 16 * h : 0;     // keys of the half that are there
+                    const int64_t off = left > 0 ? id[h] * page_bytes + head_off + ((key0 + 16 * h) & (c.page - 1)) * D : 0;
+                    const uint8_t *ks = c.k + off + lane * 16, *vs = c.v + off + lane * 16;
+#pragma unroll
+                    for (int n = 0; n < kChunks / 2; ++n) {
+                        constexpr int kKeys = 32 / kChunks;                    // keys of one copy of the warp
+                        const bool in = n * kKeys + lane / kChunks < left;
+                        const uint32_t to = dst + (h * kChunks / 2 + n) * 512;
+                        const uint32_t at_x = D == 128 && (n & 1) ? to ^ 64u : to;
+                        cp_async16_zfill(at_x, ks + n * 512, in);
+                        cp_async16_zfill(at_x + kTileKeys * D, vs + n * 512, in);
+                    }
                 }
                 if (lane < 4) {
                     const int page = lane & 1 ? id[1] : id[0];
@@ -280,46 +289,30 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
                 }
             }
 
-            // ---- scores in log2 units, masked
+            // ---- scores in log2 units: one factor a half, or capped, biased and masked one by one
             const bool masked = key0 < lo_max || key0 + kTileKeys > hi_min || bad;
+            const bool slow = masked || a.softcap > 0.f || a.slopes;
             const float ksc[2] = {clean_scale(sc.x), clean_scale(sc.y)};
             const float vsc[2] = {clean_scale(sc.z), clean_scale(sc.w)};
+            if (slow) {
+                const float up = a.softcap * kLog2e;
+                const float to2 = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e;
 #pragma unroll
-            for (int r2 = 0; r2 < 2 * MT; ++r2) {
-                const int mt = r2 / 2, e0 = 2 * (r2 & 1);
-                if (a.softcap > 0.f) {
-                    const float up = a.softcap * kLog2e;
-#pragma unroll
-                    for (int nt = 0; nt < 4; ++nt) {
-                        const float y = fac[r2] * ksc[nt / 2] * (2.f * kLog2e / a.softcap);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) s[mt][nt][e0 + e] = up * tanh_score(s[mt][nt][e0 + e] * y);
-                    }
-                } else {
+                for (int r2 = 0; r2 < 2 * MT; ++r2) {
+                    const int mt = r2 / 2, e0 = 2 * (r2 & 1);
 #pragma unroll
                     for (int nt = 0; nt < 4; ++nt) {
-                        const float y = fac[r2] * ksc[nt / 2] * kLog2e;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) s[mt][nt][e0 + e] *= y;
-                    }
-                }
-                if (a.slopes) {
-#pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
+                        const float y = fac[r2] * ksc[nt / 2] * to2;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int key = key0 + nt * 8 + perm<D>(2 * qc + e);
-                            s[mt][nt][e0 + e] -= slope[r2] * fabsf((float)(pos[r2] - key));
+                            float x = s[mt][nt][e0 + e] * y;
+                            if (a.softcap > 0.f) x = up * tanh_score(x);
+                            if (a.slopes) x -= slope[r2] * fabsf((float)(pos[r2] - key));
+                            const bool gone = key < lo[r2] || key >= hi[r2] || (bad >> (nt / 2) & 1);
+                            s[mt][nt][e0 + e] = gone ? -INFINITY : x;
                         }
-                }
-                if (masked) {
-#pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = key0 + nt * 8 + perm<D>(2 * qc + e);
-                            if (key < lo[r2] || key >= hi[r2] || (bad >> (nt / 2) & 1)) s[mt][nt][e0 + e] = -INFINITY;
-                        }
+                    }
                 }
             }
 
@@ -333,9 +326,14 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
 #pragma unroll
             for (int r2 = 0; r2 < 2 * MT; ++r2) {
                 const int mt = r2 / 2, e0 = 2 * (r2 & 1);
-                float mx = -INFINITY;
+                float f[2], mx = -INFINITY;
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(s[mt][nt][e0], s[mt][nt][e0 + 1]));
+                for (int hf = 0; hf < 2; ++hf) {
+                    f[hf] = slow ? 1.f : fac[r2] * ksc[hf] * kLog2e;
+                    const float top = fmaxf(fmaxf(s[mt][2 * hf][e0], s[mt][2 * hf][e0 + 1]),
+                                            fmaxf(s[mt][2 * hf + 1][e0], s[mt][2 * hf + 1][e0 + 1]));
+                    mx = fmaxf(mx, top * f[hf]);
+                }
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float m_new = fmaxf(m[r2], mx);
@@ -350,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float x = s[mt][nt][e0 + e];
-                        const float p = exp2_fast(x - bias);
+                        const float p = exp2_fast(fmaf(x, f[nt / 2], -bias));
                         sum += p;
                         // a key that is not seen weighs 0 even in a page whose scale is NaN
                         s[mt][nt][e0 + e] = x == -INFINITY ? 0.f : p * vrel[nt / 2];

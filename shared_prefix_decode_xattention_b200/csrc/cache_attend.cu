@@ -292,8 +292,13 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
             // ---- scores in log2 units: one factor a half, or capped, biased and masked one by one
             const bool masked = key0 < lo_max || key0 + kTileKeys > hi_min || bad;
             const bool slow = masked || a.softcap > 0.f || a.slopes;
-            const float ksc[2] = {clean_scale(sc.x), clean_scale(sc.y)};
-            const float vsc[2] = {clean_scale(sc.z), clean_scale(sc.w)};
+            float ksc[2] = {sc.x, sc.y}, vsc[2] = {sc.z, sc.w};
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+                if (!(ksc[hf] + vsc[hf] < INFINITY)) {   // a scale that is no number: every score of the half is NaN,
+                    ksc[hf] = __int_as_float(0x7fc00000);   // and a key that is not seen still weighs 0
+                    vsc[hf] = 0.f;
+                }
             if (slow) {
                 const float up = a.softcap * kLog2e;
                 const float to2 = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e;
@@ -309,15 +314,23 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
                             float x = s[mt][nt][e0 + e] * y;
                             if (a.softcap > 0.f) x = up * tanh_score(x);
                             if (a.slopes) x -= slope[r2] * fabsf((float)(pos[r2] - key));
-                            const bool gone = key < lo[r2] || key >= hi[r2] || (bad >> (nt / 2) & 1);
-                            s[mt][nt][e0 + e] = gone ? -INFINITY : x;
+                            s[mt][nt][e0 + e] = x;
                         }
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = key0 + nt * 8 + perm<D>(2 * qc + e);
+                                if (key < lo[r2] || key >= hi[r2] || (bad >> (nt / 2) & 1)) s[mt][nt][e0 + e] = -INFINITY;
+                            }
                     }
                 }
             }
 
             // ---- running maximum, weights
-            const float vnew = fmaxf(vref, fmaxf(vsc[0], vsc[1]));   // (fmaxf passes over a NaN)
+            const float vnew = fmaxf(vref, fmaxf(vsc[0], vsc[1]));
             const float vdown = vref / vnew;
             const float vrel[2] = {vsc[0] / vnew, vsc[1] / vnew};
             float alpha[2 * MT];
@@ -347,11 +360,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
                 for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float x = s[mt][nt][e0 + e];
-                        const float p = exp2_fast(fmaf(x, f[nt / 2], -bias));
+                        const float p = exp2_fast(fmaf(s[mt][nt][e0 + e], f[nt / 2], -bias));
                         sum += p;
-                        // a key that is not seen weighs 0 even in a page whose scale is NaN
-                        s[mt][nt][e0 + e] = x == -INFINITY ? 0.f : p * vrel[nt / 2];
+                        s[mt][nt][e0 + e] = p * vrel[nt / 2];
                     }
                 l[r2] = l[r2] * alpha[r2] + sum;
             }

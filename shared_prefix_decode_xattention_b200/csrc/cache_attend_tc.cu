@@ -43,7 +43,8 @@ constexpr uint32_t kTmemCols = 512;            // S0 [0,128) S1 [128,256) O0 [25
 constexpr float kMinLogV = -100.f;             // log2 of the smallest V scale told from 0
 
 struct Scales {
-    float k[8], lv[8], iv[8];   // by 16 keys: K scale, log2 V scale, 1 / V scale
+    float2 k[8];                // by 16 keys: K scale, log2 V scale
+    float iv[8];                // 1 / V scale
     int bad;                    // bit g: group g lies in a page that is not there; bit 8: a V scale is NaN
     int pad[3];
 };
@@ -58,7 +59,8 @@ struct Lay {
     static constexpr uint32_t raw = 6 * kTile;                // codes of the next K and V chunk (first the plan's scratch)
     static constexpr uint32_t sc = raw + 2 * kChunk * D;
     static constexpr uint32_t x = sc + kRing * sizeof(Scales);   // [128] (M, l) of a narrow segment's second half
-    static constexpr uint32_t bar = x + 1024;
+    static constexpr uint32_t unit = x + 1024;
+    static constexpr uint32_t bar = unit + 64;
     static constexpr uint32_t misc = bar + 256;
     static constexpr uint32_t total = misc + 16 + 1024;       // with room to align the window
 };
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
     volatile int *abort = reinterpret_cast<int *>(base + L::misc + 4);
     Scales *ring = reinterpret_cast<Scales *>(base + L::sc);
     float2 *xch = reinterpret_cast<float2 *>(base + L::x);
+    float2 *unit = reinterpret_cast<float2 *>(base + L::unit);   // [8] (1, 0)
     const CacheArgs &c = a.c;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
@@ -128,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         mbar_init(bar(B_XCH), 128);
         mbar_init(bar(B_XDONE), 128);
         mbar_init(bar(B_DONE), 1);
+        for (int i = 0; i < 8; ++i) unit[i] = make_float2(1.f, 0.f);
         *abort = 0;
         fence_mbar_init();
     }
@@ -236,24 +240,22 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                         const uint32_t below = r0 >= 32 ? ~0u : r0 <= 0 ? 0u : (1u << r0) - 1u;
                         const uint32_t till = r1 >= 32 ? ~0u : r1 <= 0 ? 0u : (1u << r1) - 1u;
                         uint32_t seen = till & ~below;
-                        float2 kk = *reinterpret_cast<const float2 *>(&sc.k[2 * p]);
-                        kk.x *= f0;
-                        kk.y *= f0;
-                        const float2 vv = *reinterpret_cast<const float2 *>(&sc.lv[2 * p]);
+                        const float2 g0 = sc.k[2 * p], g1 = sc.k[2 * p + 1];
+                        const float k0 = g0.x * f0, k1 = g1.x * f0;
                         if (bad >> (2 * p) & 1) seen &= 0xffff0000u;
                         if (bad >> (2 * p + 1) & 1) seen &= 0x0000ffffu;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            float y = x[32 * p + e] * (e < 16 ? kk.x : kk.y);
+                            float y = x[32 * p + e] * (e < 16 ? k0 : k1);
                             if (capped) y = up * tanh_score(y);
                             if (a.slopes) y -= slope * fabsf(away - (float)(32 * p + e));
-                            x[32 * p + e] = seen >> e & 1 ? y + (e < 16 ? vv.x : vv.y) : -INFINITY;
+                            x[32 * p + e] = seen >> e & 1 ? y + (e < 16 ? g0.y : g1.y) : -INFINITY;
                         }
                     }
                 }
-                // t = factor * x + offset is a weight's exponent (x itself after the slow way)
-                auto factor = [&](int g) { return slow ? 1.f : sc.k[g] * f0; };
-                auto offset = [&](int g) { return slow ? 0.f : sc.lv[g]; };
+                // t = fo.x f1 x + fo.y is a weight's exponent (x itself after the slow way)
+                const float2 *fo = slow ? unit : sc.k;
+                const float f1 = slow ? 1.f : f0;
                 // ---- the largest weight's exponent, the row's reference
                 float top = -INFINITY;
 #pragma unroll
@@ -261,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                     float m = fmaxf(x[16 * g], x[16 * g + 1]);
 #pragma unroll
                     for (int e = 2; e < 16; e += 2) m = tc::fmax3(m, x[16 * g + e], x[16 * g + e + 1]);
-                    top = fmaxf(top, fmaf(m, factor(g), offset(g)));
+                    const float2 kv = fo[g];
+                    top = fmaxf(top, fmaf(m, kv.x * f1, kv.y));
                 }
                 const bool raise = top > M + 8.f || (M == -INFINITY && top > -INFINITY);
                 float alpha = 1.f;
@@ -288,18 +291,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                     uint32_t w[32];
 #pragma unroll
                     for (int g = 4 * q; g < 4 * q + 4; ++g) {
-                        const float fg = factor(g), dg = offset(g) - ref;
+                        const float2 kv = fo[g];
+                        const float fg = kv.x * f1, dg = kv.y - ref;
                         const float2 ff = make_float2(fg, fg), dd = make_float2(dg, dg);
-                        float s0 = 0.f, s1 = 0.f;
+                        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             const float2 t = tc::ffma2(make_float2(x[16 * g + e], x[16 * g + e + 1]), ff, dd);
-                            const float p0 = exp2_fast(t.x), p1 = exp2_fast(t.y);
-                            s0 += p0;
-                            s1 += p1;
-                            w[8 * (g & 3) + e / 2] = pack_f16(p0, p1);
+                            const float2 p = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+                            sum = tc::fadd2(sum, p);
+                            w[8 * (g & 3) + e / 2] = pack_f16(p.x, p.y);
                         }
-                        s0 += s1;
+                        const float s0 = sum.x + sum.y;
                         l += s0 == 0.f ? 0.f : s0 * sc.iv[g];
                     }
                     __syncwarp();
@@ -420,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
             const Seg s = segment(a, cur, end - at);
             const int32_t *line = c.table + (int64_t)cur.r * c.max_pages;
-            // lane g of every warp holds the page of group g % 8 of a chunk (-2: no keys, -1: no such page)
+            // Lane g of every warp holds group g % 8 of a chunk: its page (-2: no keys, -1: no such page), and where its
+            // 16 keys lie, in blocks of 16 keys (they are contiguous in a page and head).
             auto ids_of = [&](int ch) {
                 const int key = s.kb0 + ch * kChunk + 16 * (lane & 7);
                 int id = -2;
@@ -433,18 +437,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 }
                 return id;
             };
+            auto block_of = [&](int ch, int id) {
+                const int key = s.kb0 + ch * kChunk + 16 * (lane & 7);
+                return id < 0 ? -1 : (id * c.Hkv + cur.g) * (c.page / 16) + (key & (c.page - 1)) / 16;
+            };
             // a thread's codes wait in shared memory of its own (16 bytes of each pass)
             const uint32_t raw = L::raw + 16u * t;
-            auto load = [&](const uint8_t *src, uint32_t to, int ch, int ids) {
+            auto load = [&](const uint8_t *src, uint32_t to, int ch, int block) {
                 if (ch < s.chunks) {
+                    const int left = s.ke - s.kb0 - ch * kChunk - key_in;      // keys from this thread's first one on
+                    const uint8_t *from = src + ((key_in % 16) * D + ck * 16);
 #pragma unroll
                     for (int i = 0; i < kPass; ++i) {
-                        const int kl = i * kRows + key_in;
-                        const int key = s.kb0 + ch * kChunk + kl;
-                        const int id = __shfl_sync(0xffffffffu, ids, kl / 16);
-                        const bool in = id >= 0 && key < s.ke;
-                        const int64_t off = (((int64_t)id * c.Hkv + cur.g) * c.page + (key & (c.page - 1))) * D + ck * 16;
-                        cp_async16_zfill(sb + to + i * (kConvThreads * 16), src + (in ? off : 0), in);
+                        const int b = __shfl_sync(0xffffffffu, block, (i * kRows + key_in) / 16);
+                        const bool in = b >= 0 && i * kRows < left;
+                        cp_async16_zfill(sb + to + i * (kConvThreads * 16), from + (int64_t)(in ? b : 0) * (16 * D), in);
                     }
                 }
                 cp_async_commit();
@@ -465,8 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             };
             const uint32_t raw_v = raw + kChunk * D;
             int ids = ids_of(0), next = ids_of(1);
-            load(c.k, raw, 0, ids);
-            load(c.v, raw_v, 0, ids);
+            int block = block_of(0, ids);
+            load(c.k, raw, 0, block);
+            load(c.v, raw_v, 0, block);
             for (int ch = 0; ch < s.chunks; ++ch) {
                 const int gi = gc + ch, st = gi & 1;
                 const int ids2 = next;
@@ -486,8 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                     const uint32_t gone = __ballot_sync(0xffffffffu, ids == -1) & 255u;
                     const uint32_t sick = __ballot_sync(0xffffffffu, vs != vs || ks != ks) & 255u;
                     if (lane < 8) {
-                        sc.k[lane] = ks;
-                        sc.lv[lane] = lv;
+                        sc.k[lane] = make_float2(ks, lv);
                         sc.iv[lane] = exp2f(-lv);
                     }
                     if (lane == 0) sc.bad = (int)gone | (sick ? 256 : 0);
@@ -497,13 +504,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 cp_async_wait_group<1>();
                 put(L::k + st * L::kTile, raw);
                 mbar_arrive(bar(B_KFULL + st));
-                load(c.k, raw, ch + 1, ids2);
+                block = block_of(ch + 1, ids2);
+                load(c.k, raw, ch + 1, block);
                 if (gi >= 2) ok = mbar_wait(bar(B_VEMPTY + st), ((gi >> 1) - 1) & 1, abort);
                 if (!ok) break;
                 cp_async_wait_group<1>();
                 put(L::v + st * L::kTile, raw_v);
                 mbar_arrive(bar(B_VFULL + st));
-                load(c.v, raw_v, ch + 1, ids2);
+                load(c.v, raw_v, ch + 1, block);
                 ids = ids2;
             }
             gc += s.chunks;
@@ -517,6 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         if (warp == 12) {
             constexpr uint32_t idS = tc::idesc_f16(128, 128, false), idO = tc::idesc_f16(128, D, true);
             int gc = 0, cnt0 = 0, cnt1 = 0, nq0 = 0, nq1 = 0;
+            const uint64_t dq = tc::desc(sb + L::q, 16, 1024), dk = tc::desc(sb + L::k, 16, 1024);
+            const uint64_t dv = tc::desc(sb + L::v, L::kHalf, 1024);
             bool ok = true;
             for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
                 const Seg s = segment(a, cur, end - at);
@@ -540,12 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                                 if (mbar_test(bar(B_PFULL + h), (cnt[h] + ip[h]) & 1) &&
                                     mbar_test(bar(B_VFULL + st), (gi >> 1) & 1)) {
                                     tc::fence_after();
-                                    const uint32_t kv = sb + L::v + st * L::kTile;
+                                    const uint64_t v = dv + st * (L::kTile >> 4);
 #pragma unroll
                                     for (int k = 0; k < 8; ++k)
-                                        tc::mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 8u * k,
-                                                   tc::desc(kv + (uint32_t)k * 2048u, L::kHalf, 1024), idO,
-                                                   (k > 0 || ip[h] > 0) ? 1u : 0u);
+                                        tc::mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 8u * k, v + k * (2048 >> 4),
+                                                   idO, (k > 0 || ip[h] > 0) ? 1u : 0u);
                                     tc::commit(bar(B_PVDONE + h));
                                     tc::commit(bar(B_VEMPTY + st));
                                     if (alone) tc::commit(bar(B_VEMPTY + st));
@@ -558,13 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                                 const int gi = gc + s.chunk_of(h, is[h]), st = gi & 1;
                                 if (mbar_test(bar(B_KFULL + st), (gi >> 1) & 1)) {
                                     tc::fence_after();
-                                    const uint32_t kq = sb + L::q + (s.narrow ? 0 : h) * L::kTile;
-                                    const uint32_t kk = sb + L::k + st * L::kTile;
+                                    const uint64_t q = dq + (s.narrow ? 0 : h) * (L::kTile >> 4);
+                                    const uint64_t kk = dk + st * (L::kTile >> 4);
 #pragma unroll
                                     for (int k = 0; k < D / 16; ++k) {
-                                        const uint32_t off = (uint32_t)(k >> 2) * L::kHalf + (uint32_t)(k & 3) * 32u;
-                                        tc::mma_ss(tmem + 128u * h, tc::desc(kq + off, 16, 1024),
-                                                   tc::desc(kk + off, 16, 1024), idS, k > 0);
+                                        const uint32_t off = ((uint32_t)(k >> 2) * L::kHalf + (uint32_t)(k & 3) * 32u) >> 4;
+                                        tc::mma_ss(tmem + 128u * h, q + off, kk + off, idS, k > 0);
                                     }
                                     tc::commit(bar(B_SFULL + h));
                                     tc::commit(bar(B_KEMPTY + st));

@@ -173,22 +173,39 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             const int n = s.tile_chunks(h);
             const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
             const int pos = s.row.len - s.row.n + tok;
-            // ---- the warp's 32 query rows as fp16, near 1: D / 8 lanes a row, so that loads are whole lines
+            // ---- the warp's 32 query rows as fp16, near 1: copied into their places in the operand (D / 8 lanes a row,
+            // whole lines), then scaled there.  (Loops stay rolled: this code runs once a segment, and fetching
+            // instructions that are not in the caches costs more than they do.)
             float fac = 0.f;
-            if (n > 0 || (s.narrow && s.chunks > 0)) {
-                constexpr int kPer = 256 / D;          // rows of one load of the warp
+            if (s.chunks > 0 && (n > 0 || s.narrow)) {
+                constexpr int kPer = 256 / D;          // rows of one copy of the warp
                 const int64_t q_off = valid ? (int64_t)(s.row.t0 + tok) * a.q_stride + (int64_t)head * D : -1;
                 const int ln = lane % (D / 8);
-                uint4 v[32 / kPer];                    // all loads in flight at once
-#pragma unroll
-                for (int i = 0; i < 32 / kPer; ++i) {
-                    const int64_t off = __shfl_sync(0xffffffffu, q_off, i * kPer + lane / (D / 8));
-                    v[i] = off >= 0 ? *reinterpret_cast<const uint4 *>(a.q + off + 8 * ln) : make_uint4(0, 0, 0, 0);
+                const uint32_t qt = (s.narrow ? 0 : h) * L::kTile;
+                if (!s.narrow || h == 0) {
+#pragma unroll 1
+                    for (int i = 0; i < 32 / kPer; ++i) {
+                        const int rr = i * kPer + lane / (D / 8);
+                        const int64_t off = __shfl_sync(0xffffffffu, q_off, rr);
+                        cp_async16_zfill(sb + L::q + qt + sw128<D>(32 * (warp & 3) + rr, ln), a.q + (off >= 0 ? off + 8 * ln : 0),
+                                         off >= 0);
+                    }
+                    cp_async_commit();
+                    cp_async_wait_all();
+                    __syncwarp();
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 32 / kPer; ++i) {
+                    const int rr = i * kPer + lane / (D / 8);
+                    uint4 v;
+                    if (!s.narrow || h == 0) {
+                        v = *reinterpret_cast<const uint4 *>(base + L::q + qt + sw128<D>(32 * (warp & 3) + rr, ln));
+                    } else {   // (the other warpgroup's rows: only their scale is needed)
+                        const int64_t off = __shfl_sync(0xffffffffu, q_off, rr);
+                        v = off >= 0 ? *reinterpret_cast<const uint4 *>(a.q + off + 8 * ln) : make_uint4(0, 0, 0, 0);
+                    }
                     float f[8], top = 0.f;
-                    unpack8(v[i], f);
+                    unpack8(v, f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
 #pragma unroll
@@ -198,8 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                     if (lane / kPer == i) fac = mine;
                     if (!s.narrow || h == 0) {
                         const float down = pow2i(-ex);
-                        const int rr = 32 * (warp & 3) + i * kPer + lane / (D / 8);
-                        *reinterpret_cast<uint4 *>(base + L::q + h * L::kTile + sw128<D>(rr, ln)) =
+                        *reinterpret_cast<uint4 *>(base + L::q + qt + sw128<D>(32 * (warp & 3) + rr, ln)) =
                             make_uint4(pack_f16(f[0] * down, f[1] * down), pack_f16(f[2] * down, f[3] * down),
                                        pack_f16(f[4] * down, f[5] * down), pack_f16(f[6] * down, f[7] * down));
                     }
@@ -350,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 auto slot = [&](int row, int ch) { return stage + row * (2 * D) + ((ch ^ (row & 7)) << 4); };
                 auto flush = [&](uint8_t *dst, int64_t row_bytes, int64_t my_row) {   // lane's row of the result (-1: none)
                     __syncwarp();
-#pragma unroll 4
+#pragma unroll 2
                     for (int i = 0; i < D / 8; ++i) {
                         const int rr = i * (256 / D) + lane / (D / 8), ch = lane % (D / 8);
                         const int64_t row = __shfl_sync(0xffffffffu, my_row, rr);

@@ -237,21 +237,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                      mbar_wait(bar(B_SFULL + h), (cnt + i) & 1, abort);
                 if (!ok) break;
                 tc::fence_after();
-                float x[128];
-#pragma unroll
-                for (int p = 0; p < 4; ++p) tc::ld32(ts + 32u * p, x + 32 * p);
                 const Scales &sc = ring[gi % kRing];
                 const int key0 = s.kb0 + ch * kChunk;
                 const int bad = sc.bad;
                 const bool masked = key0 < lo_max || key0 + kChunk > hi_min || bad;
                 const bool slow = masked || capped || a.slopes;
-#pragma unroll
-                for (int p = 0; p < 4; ++p) tc::wait_ld_into(x + 32 * p);
+                // Scores to exponents of weights, in place.  (Rolled: this and the body below, both unrolled, are longer
+                // than the instruction caches next to the schedulers, and waiting for instructions cost more than the
+                // second reading: 374 against 342 us for capped, masked chunks of 3700 tokens.)
                 if (slow) {
                     const float up = a.softcap * kLog2e;
                     const float away = (float)(pos - key0);
-#pragma unroll
+#pragma unroll 1
                     for (int p = 0; p < 4; ++p) {
+                        float x[32];
+                        tc::ld32(ts + 32u * p, x);
                         const int r0 = vis.lo - key0 - 32 * p, r1 = vis.hi - key0 - 32 * p;
                         const uint32_t below = r0 >= 32 ? ~0u : r0 <= 0 ? 0u : (1u << r0) - 1u;
                         const uint32_t till = r1 >= 32 ? ~0u : r1 <= 0 ? 0u : (1u << r1) - 1u;
@@ -260,15 +260,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                         const float k0 = g0.x * f0, k1 = g1.x * f0;
                         if (bad >> (2 * p) & 1) seen &= 0xffff0000u;
                         if (bad >> (2 * p + 1) & 1) seen &= 0x0000ffffu;
+                        const float away_p = away - 32.f * p;
+                        tc::wait_ld_into(x);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            float y = x[32 * p + e] * (e < 16 ? k0 : k1);
+                            float y = x[e] * (e < 16 ? k0 : k1);
                             if (capped) y = up * tanh_score(y);
-                            if (a.slopes) y -= slope * fabsf(away - (float)(32 * p + e));
-                            x[32 * p + e] = seen >> e & 1 ? y + (e < 16 ? g0.y : g1.y) : -INFINITY;
+                            if (a.slopes) y -= slope * fabsf(away_p - (float)e);
+                            x[e] = seen >> e & 1 ? y + (e < 16 ? g0.y : g1.y) : -INFINITY;
                         }
+                        __syncwarp();
+                        tc::st32(ts + 32u * p, reinterpret_cast<const uint32_t *>(x));
                     }
+                    tc::wait_st();
                 }
+                float x[128];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) tc::ld32(ts + 32u * p, x + 32 * p);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) tc::wait_ld_into(x + 32 * p);
                 // t = fo.x f1 x + fo.y is a weight's exponent (x itself after the slow way)
                 const float2 *fo = slow ? unit : sc.k;
                 const float f1 = slow ? 1.f : f0;

@@ -568,19 +568,14 @@ __global__ void __launch_bounds__(128) cache_tile_lo_kernel(AttendArgs a, int R,
     griddep_launch_dependents();
     const int64_t slot = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
     if (slot >= slots) return;
-    int lo = 0, hi = a.c.n_rows - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (tile_slot(a, mid, R) <= slot) lo = mid;
-        else hi = mid - 1;
-    }
-    const RowSpan row = row_span(a.c, lo, a.max_q);
-    const int64_t t = slot - tile_slot(a, lo, R);
+    int r;
+    int64_t t;
+    const RowSpan row = slot_tile(a, R, slot, r, t);
     if (t < 0 || t >= row_tiles(a, row, R)) return;
     const int i0 = (int)(t * R / a.G), i1 = (int)((min((t + 1) * R, (int64_t)row.n * a.G) - 1) / a.G);
     int low = row.len;
     for (int i = i0 + (int)(threadIdx.x % 32); i <= i1; i += 32) {
-        const KeyRange q = query_keys(a, row, lo, i);
+        const KeyRange q = query_keys(a, row, r, i);
         if (q.lo < q.hi) low = min(low, q.lo);
     }
     low = __reduce_min_sync(0xffffffffu, low);

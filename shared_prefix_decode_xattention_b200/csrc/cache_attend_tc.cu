@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
             const int pos = s.row.len - s.row.n + tok;
             // ---- the warp's 32 query rows as fp16, near 1: copied into their places in the operand (D / 8 lanes a row,
-            // whole lines), then scaled there.  (Loops stay rolled: this code runs once a segment, and fetching
+            // whole lines), then scaled there.  (Loops stay mostly rolled: this code runs once a segment, and fetching
             // instructions that are not in the caches costs more than they do.)
             float fac = 0.f;
             if (s.chunks > 0 && (n > 0 || s.narrow)) {
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 const int ln = lane % (D / 8);
                 const uint32_t qt = (s.narrow ? 0 : h) * L::kTile;
                 if (!s.narrow || h == 0) {
-#pragma unroll 1
+#pragma unroll 4
                     for (int i = 0; i < 32 / kPer; ++i) {
                         const int rr = i * kPer + lane / (D / 8);
                         const int64_t off = __shfl_sync(0xffffffffu, q_off, rr);
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                     cp_async_wait_all();
                     __syncwarp();
                 }
-#pragma unroll 1
+#pragma unroll 4
                 for (int i = 0; i < 32 / kPer; ++i) {
                     const int rr = i * kPer + lane / (D / 8);
                     uint4 v;
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 auto slot = [&](int row, int ch) { return stage + row * (2 * D) + ((ch ^ (row & 7)) << 4); };
                 auto flush = [&](uint8_t *dst, int64_t row_bytes, int64_t my_row) {   // lane's row of the result (-1: none)
                     __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
                     for (int i = 0; i < D / 8; ++i) {
                         const int rr = i * (256 / D) + lane / (D / 8), ch = lane % (D / 8);
                         const int64_t row = __shfl_sync(0xffffffffu, my_row, rr);

@@ -42,11 +42,15 @@ struct KeyRange {
     int lo, hi;
 };
 
-// Where d_first is given, the lowest key that a tile's queries see is worked out
-// by a kernel of its own first, into one slot a tile: row r's tiles begin at
-// tile_slot (no row has more tiles than the gap to the next row's slots).
+// The tiles of all rows are numbered with gaps: row r's begin at tile_slot (no
+// row has more tiles than the gap to the next row's), so a slot's row is found
+// from d_cu alone and the plan runs over slots, one or a few a thread, however
+// the tokens are spread.  R is a power of two.
 __device__ __forceinline__ int64_t tile_slot(const AttendArgs &a, int r, int R) {
-    return (int64_t)a.c.cu[r] * a.G / R + r;
+    return ((int64_t)a.c.cu[r] * a.G >> (31 - __clz(R))) + r;
+}
+__device__ __forceinline__ int64_t tile_slots(const AttendArgs &a, int R) {
+    return ((int64_t)a.c.n_tokens * a.G >> (31 - __clz(R))) + a.c.n_rows;
 }
 
 // The keys [lo, hi) that some query of tile t of a row with span s may see.
@@ -73,11 +77,23 @@ __device__ __forceinline__ int row_tiles(const AttendArgs &a, const RowSpan &s, 
     return (int)(((int64_t)s.n * a.G + R - 1) / R);
 }
 
-__device__ __forceinline__ int64_t row_units(const AttendArgs &a, const RowSpan &s, int r, int R) {
-    const int tiles = row_tiles(a, s, R);
-    int64_t u = 0;
-    for (int t = 0; t < tiles; ++t) u += range_units(a, tile_keys(a, s, r, R, t));
-    return u * a.c.Hkv;
+// The row and tile of a slot (t past the row's tiles: an empty slot).
+__device__ __forceinline__ RowSpan slot_tile(const AttendArgs &a, int R, int64_t slot, int &r, int64_t &t) {
+    int lo = 0, hi = a.c.n_rows - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (tile_slot(a, mid, R) <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    r = lo;
+    t = slot - tile_slot(a, lo, R);
+    return row_span(a.c, lo, a.max_q);
+}
+
+// Units of one kv head of a slot's tile (0: an empty slot).
+__device__ __forceinline__ int slot_units(const AttendArgs &a, int R, int64_t slot, int &r, int64_t &t) {
+    const RowSpan s = slot_tile(a, R, slot, r, t);
+    return t >= 0 && t < row_tiles(a, s, R) ? range_units(a, tile_keys(a, s, r, R, (int)t)) : 0;
 }
 
 // Shared memory of plan_begin.
@@ -95,12 +111,16 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_u
                                            int64_t &per) {
     int64_t *base = sm.base;
     Cursor &first = sm.first;
-    const int n_rows = a.c.n_rows;
-    const int rpt = (n_rows + T - 1) / T;
-    const int r0 = min((int)threadIdx.x * rpt, n_rows), r1 = min(r0 + rpt, n_rows);
+    const int64_t slots = tile_slots(a, R), spt = (slots + T - 1) / T;
+    const int64_t s0 = min(threadIdx.x * spt, slots), s1 = min(s0 + spt, slots);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += row_units(a, row_span(a.c, r, a.max_q), r, R);
+    int units = 0, r = 0;
+    int64_t t = 0;
+    for (int64_t s = s0; s < s1; ++s) {
+        units = slot_units(a, R, s, r, t);
+        mine += (int64_t)units * a.c.Hkv;
+    }
     int64_t x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -114,7 +134,7 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_u
         for (int i = 0; i < T / 32; ++i) base[i + 1] += base[i];
     __syncthreads();
     const int64_t total = base[T / 32];
-    const int64_t from = base[warp] + x - mine;   // first unit of this thread's rows
+    const int64_t from = base[warp] + x - mine;   // first unit of this thread's slots
     per = max((int64_t)min_units, (total + gridDim.x - 1) / gridDim.x);
     begin = blockIdx.x * per;
     end = min(begin + per, total);
@@ -125,23 +145,16 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_u
     }
     if (from <= begin && begin < from + mine) {
         int64_t left = begin - from;
-        int r = r0;
-        for (; r < r1 - 1; ++r) {
-            const int64_t u = row_units(a, row_span(a.c, r, a.max_q), r, R);
-            if (left < u) break;
-            left -= u;
-        }
-        const RowSpan s = row_span(a.c, r, a.max_q);
-        const int tiles = row_tiles(a, s, R);
-        int t = 0, units = 1;
-        for (; t < tiles; ++t) {
-            units = range_units(a, tile_keys(a, s, r, R, t));
-            if (left < (int64_t)units * a.c.Hkv) break;
-            left -= (int64_t)units * a.c.Hkv;
-        }
+        if (spt > 1)                              // (one slot: it is at hand)
+            for (int64_t s = s0; s < s1; ++s) {
+                units = slot_units(a, R, s, r, t);
+                if (left < (int64_t)units * a.c.Hkv) break;
+                left -= (int64_t)units * a.c.Hkv;
+            }
+        units = max(units, 1);
         first.r = r;
-        first.t = t;
-        first.g = (int)(left / units);
+        first.t = (int)t;
+        first.g = min((int)(left / units), a.c.Hkv - 1);
         first.u = (int)(left % units);
         first.units = units;
         if (p.first) p.first[blockIdx.x] = first;

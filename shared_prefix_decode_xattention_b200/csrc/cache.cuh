@@ -62,6 +62,7 @@ struct AttendArgs {
     const int32_t *prefix;
     const int32_t *first;
     int whole;                  // 1: a work unit is a whole segment (every row is short)
+    int lead;                   // units that stand for a segment's cost beside its keys
     int32_t *tile_lo;           // lowest visible key of each tile (with first)
     uint8_t *ws;
 };

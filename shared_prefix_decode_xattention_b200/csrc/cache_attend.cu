@@ -84,8 +84,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
     griddep_wait();
     griddep_launch_dependents();
     Cursor cur;
-    int64_t begin, end, per;
-    if (!plan_begin<kThreads>(a, R, min_units, sm.plan, po, cur, begin, end, per)) return;
+    NoParts units;
+    int64_t begin, end;
+    if (!plan_begin<kThreads>(a, R, min_units, sm.plan, po, units, cur, begin, end)) return;
 
     const uint32_t ring0 = smem_u32(&sm.ring[warp][0][0]);
     const uint32_t sc0 = smem_u32(&sm.sc[warp][0][0]);
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
     for (int64_t at = begin; at < end;) {
         const RowSpan row = row_span(c, cur.r, a.max_q);
         const int u1 = (int)min((int64_t)cur.units, cur.u + (end - at));
-        const KeyRange sk = segment_keys(a, row, cur, u1, R);
+        const KeyRange sk = segment_keys(a, units, row, cur, u1, R);
         int kb = sk.lo, ke = sk.hi;
 
         // ---- this lane's query rows: qr + 8 i of each 16-row tile
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
         }
         __syncthreads();   // the rings and (m, l) are free for the next segment
         at += u1 - cur.u;
-        if (at < end) plan_next(a, R, cur);
+        if (at < end) plan_next(a, units, R, cur);
         if (cur.r >= c.n_rows) break;
     }
 }
@@ -507,12 +508,22 @@ __global__ void __launch_bounds__(128) cache_join_kernel(AttendArgs a, int R, Pl
     griddep_launch_dependents();
     const Cursor cur = po.first[blockIdx.x];
     if (cur.u == 0) return;
-    const int64_t per = *po.per;
-    const int64_t start = (int64_t)blockIdx.x * per - cur.u;     // the segment's first unit
-    const int c0 = (int)(start / per);
-    if (c0 != (int)blockIdx.x - 1) return;
-    const int n = (int)((start + cur.units - 1) / per) - c0 + 1;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    auto inside = [&](int c) {                      // CTA c begins in the middle of the same segment
+        if (c >= (int)gridDim.x) return false;
+        const Cursor f = po.first[c];
+        return f.u > 0 && f.r == cur.r && f.t == cur.t && f.g == cur.g;
+    };
+    const int c0 = blockIdx.x - 1;                  // (CTA 0 begins at a segment's start)
+    if (inside(c0)) return;
+    int n = 2;                                      // parts: CTA c0's, this one's, those of the CTAs after it
+    for (;; n += 32) {
+        const uint32_t more = __ballot_sync(0xffffffffu, inside(c0 + n + lane));
+        if (more != 0xffffffffu) {
+            n += __ffs(~more) - 1;
+            break;
+        }
+    }
     const int rr = blockIdx.y * (4 / WPR) + warp / WPR, sub = warp % WPR;
     const RowSpan row = row_span(a.c, cur.r, a.max_q);
     const int ia = cur.t * R + rr;
@@ -586,18 +597,18 @@ constexpr int kSmallCtas = 3 * kSms;         // 16-row tiles: three CTAs an SM
 constexpr int kWideCtas = 2 * kSms;          // 32-row tiles: two
 constexpr int kTcRows256 = 256;              // tcgen05 tiles: one
 constexpr int kMinUnits = 4;                 // fewest units a CTA takes (512 keys): below, joining costs more than it spreads
+constexpr int kTcLead = 3;                   // a 256-row segment's rows and result cost about as much as three units
 constexpr int kWholeUnits = 8;               // rows of at most this many units are not cut
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct WsLayout {
-    size_t first, per, o, ml, lo, total;
+    size_t first, o, ml, lo, total;
 };
 WsLayout ws_layout(int D, int G, int n_rows, int n_tokens) {
     WsLayout w{};
     w.first = 0;
-    w.per = up256((size_t)kSmallCtas * sizeof(Cursor));
-    w.o = w.per + 256;
+    w.o = up256((size_t)kSmallCtas * sizeof(Cursor));
     const size_t parts = 2 * std::max<size_t>({(size_t)kSmallCtas * 16, (size_t)kWideCtas * 32, (size_t)kSms * kTcRows256});
     w.ml = w.o + up256(parts * D * 4);
     w.lo = w.ml + up256(parts * 8);
@@ -640,17 +651,17 @@ cudaError_t launch_cache_attend(const AttendArgs &in, cudaStream_t s) {
     const int64_t most = (int64_t)a.max_q * a.G;
     const int R = most <= 16 ? 16 : most <= 32 ? 32 : kTcRows256;
     const int cap = R == 16 ? kSmallCtas : R == 32 ? kWideCtas : kSms;
-    const int min_units = a.whole ? 1 : kMinUnits;
+    a.lead = R == kTcRows256 && !a.whole ? kTcLead : 0;
+    const int min_units = a.whole ? 1 : kMinUnits + a.lead;
     // no more CTAs than there can be shares of the line
     const int64_t segs = (((int64_t)c.n_tokens * a.G + R - 1) / R + c.n_rows) * c.Hkv;
-    const int64_t row_units = a.whole ? 1 : (int64_t)c.max_pages * c.page / kUnitKeys + 2;
+    const int64_t row_units = a.whole ? 1 : (int64_t)c.max_pages * c.page / kUnitKeys + 2 + a.lead;
     const int ctas = (int)std::min<int64_t>(cap, (segs * row_units + min_units - 1) / min_units);
     const WsLayout l = ws_layout(c.D, a.G, c.n_rows, c.n_tokens);
     a.tile_lo = reinterpret_cast<int32_t *>(a.ws + l.lo);
     PlanOut po{};
     if (!a.whole) {
         po.first = reinterpret_cast<Cursor *>(a.ws + l.first);
-        po.per = reinterpret_cast<int64_t *>(a.ws + l.per);
         po.o = reinterpret_cast<float *>(a.ws + l.o);
         po.ml = reinterpret_cast<float2 *>(a.ws + l.ml);
     }

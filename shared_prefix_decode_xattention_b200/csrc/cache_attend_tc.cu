@@ -86,12 +86,12 @@ struct Seg {
     __device__ int chunk_of(int h, int i) const { return narrow ? 2 * i + h : i; }
 };
 
-__device__ __forceinline__ Seg segment(const AttendArgs &a, const Cursor &cur, int64_t left) {
+__device__ __forceinline__ Seg segment(const AttendArgs &a, const Parts &w, const Cursor &cur, int64_t left) {
     constexpr int R = 256;
     Seg s;
     s.row = row_span(a.c, cur.r, a.max_q);
     s.u1 = (int)min((int64_t)cur.units, cur.u + left);
-    const KeyRange k = segment_keys(a, s.row, cur, s.u1, R);
+    const KeyRange k = segment_keys(a, w, s.row, cur, s.u1, R);
     s.kb0 = k.lo & ~(kChunk - 1);
     s.ke = k.hi;
     s.chunks = k.hi > k.lo ? (k.hi - s.kb0 + kChunk - 1) / kChunk : 0;
@@ -138,8 +138,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
     griddep_wait();
     griddep_launch_dependents();
     Cursor cur;
-    int64_t begin, end, per;
-    if (!plan_begin<kThreads>(a, R, min_units, *reinterpret_cast<PlanSmem<kThreads> *>(base + L::raw), po, cur, begin, end, per)) return;   // (of the whole block)
+    Parts &units = *reinterpret_cast<Parts *>(base + L::misc + 8);
+    int64_t begin, end;
+    if (!plan_begin<kThreads>(a, R, min_units, *reinterpret_cast<PlanSmem<kThreads> *>(base + L::raw), po, units, cur, begin, end)) return;   // (of the whole block)
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                      "r"(kTmemCols)
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         int nx = 0;        // narrow segments before
         bool ok = true;
         for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
-            const Seg s = segment(a, cur, end - at);
+            const Seg s = segment(a, units, cur, end - at);
             const int ia = cur.t * R + tr + (s.narrow ? 0 : 128 * h);
             const bool valid = ia < s.row.n * a.G;
             const int tok = valid ? ia / a.G : 0, head = cur.g * a.G + (valid ? ia % a.G : 0);
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 if (fold) mbar_arrive(bar(B_XDONE));
             }
             at += s.u1 - cur.u;
-            if (at < end) plan_next(a, R, cur);
+            if (at < end) plan_next(a, units, R, cur);
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------ codes to operands
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         int gc = 0;
         bool ok = true;
         for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
-            const Seg s = segment(a, cur, end - at);
+            const Seg s = segment(a, units, cur, end - at);
             const int32_t *line = c.table + (int64_t)cur.r * c.max_pages;
             // Lane g of every warp holds group g % 8 of a chunk: its page (-2: no keys, -1: no such page), and where its
             // 16 keys lie, in blocks of 16 keys (they are contiguous in a page and head).
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             }
             gc += s.chunks;
             at += s.u1 - cur.u;
-            if (at < end) plan_next(a, R, cur);
+            if (at < end) plan_next(a, units, R, cur);
         }
         cp_async_wait_all();
     } else {
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             const uint64_t dv = tc::desc(sb + L::v, L::kHalf, 1024);
             bool ok = true;
             for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
-                const Seg s = segment(a, cur, end - at);
+                const Seg s = segment(a, units, cur, end - at);
                 if (lane == 0 && s.chunks > 0) {
                     const int n[2] = {s.tile_chunks(0), s.tile_chunks(1)};
                     const int cnt[2] = {cnt0, cnt1};
@@ -625,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
                 gc += s.chunks;
                 at += s.u1 - cur.u;
-                if (at < end) plan_next(a, R, cur);
+                if (at < end) plan_next(a, units, R, cur);
             }
             if (lane == 0) {   // every product issued has completed before tensor memory is given back
                 tc::commit(bar(B_DONE));

@@ -15,6 +15,13 @@
 //
 // In "whole" mode (every row is short) a unit is a whole segment: nothing is
 // cut and no join runs.
+//
+// A segment also costs something before its first key (its query rows, its
+// result): AttendArgs::lead units of it stand for that, at its front, without
+// keys.  A CTA's end that would fall into them, or leave or take fewer than that
+// many units of keys, moves to the segment's edge.  Where such segments are at
+// most half as many as the CTAs, every segment is cut into equal parts of its
+// own instead, a CTA a part (a unit is then a part).
 #pragma once
 
 #include "cache.cuh"
@@ -33,7 +40,6 @@ struct Cursor {
 // Results of parts of segments, for the join (null in whole mode).
 struct PlanOut {
     Cursor *first;       // [N] each CTA's first cursor (u = 0: it cuts nothing)
-    int64_t *per;        // [1] units a CTA takes
     float *o;            // [N][2][R][D]
     float2 *ml;          // [N][2][R]
 };
@@ -68,9 +74,28 @@ __device__ __forceinline__ KeyRange tile_keys(const AttendArgs &a, const RowSpan
     return k;
 }
 
-__device__ __forceinline__ int range_units(const AttendArgs &a, const KeyRange &k) {
+// chunks of kUnitKeys keys that a range touches
+__device__ __forceinline__ int range_chunks(const KeyRange &k) {
+    return max(0, (k.hi + kUnitKeys - 1) / kUnitKeys - k.lo / kUnitKeys);
+}
+
+// What a unit is.  NoParts: kUnitKeys keys (or one of the lead).  Parts, with parts > 0: a part of a segment, `parts` of
+// them shared out beside one a segment, in proportion to its share of all `chunks`.
+struct NoParts {
+    static constexpr bool kParts = false;
+    static constexpr int parts = 0, chunks = 1;
+};
+struct Parts {
+    static constexpr bool kParts = true;
+    int parts, chunks;
+};
+
+template <typename U>
+__device__ __forceinline__ int range_units(const AttendArgs &a, const U &w, const KeyRange &k) {
     if (a.whole) return 1;
-    return max(1, (k.hi + kUnitKeys - 1) / kUnitKeys - k.lo / kUnitKeys);
+    const int n = range_chunks(k);
+    if (U::kParts && w.parts > 0) return (int)max((int64_t)1, min((int64_t)n / 2, 1 + (int64_t)n * w.parts / w.chunks));
+    return max(1, a.lead + n);
 }
 
 __device__ __forceinline__ int row_tiles(const AttendArgs &a, const RowSpan &s, int R) {
@@ -90,82 +115,17 @@ __device__ __forceinline__ RowSpan slot_tile(const AttendArgs &a, int R, int64_t
     return row_span(a.c, lo, a.max_q);
 }
 
-// Units of one kv head of a slot's tile (0: an empty slot).
-__device__ __forceinline__ int slot_units(const AttendArgs &a, int R, int64_t slot, int &r, int64_t &t) {
+// The keys of a slot's tile (false: an empty slot).
+__device__ __forceinline__ bool slot_keys(const AttendArgs &a, int R, int64_t slot, int &r, int64_t &t, KeyRange &k) {
     const RowSpan s = slot_tile(a, R, slot, r, t);
-    return t >= 0 && t < row_tiles(a, s, R) ? range_units(a, tile_keys(a, s, r, R, (int)t)) : 0;
-}
-
-// Shared memory of plan_begin.
-template <int T>
-struct PlanSmem {
-    int64_t base[T / 32 + 1];
-    Cursor first;
-};
-
-// Every thread of the block gets the block's first cursor and [begin, end)
-// (false: no work).  T = threads of the block.
-template <int T>
-__device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_units, PlanSmem<T> &sm,
-                                           const PlanOut &p, Cursor &cur, int64_t &begin, int64_t &end,
-                                           int64_t &per) {
-    int64_t *base = sm.base;
-    Cursor &first = sm.first;
-    const int64_t slots = tile_slots(a, R), spt = (slots + T - 1) / T;
-    const int64_t s0 = min(threadIdx.x * spt, slots), s1 = min(s0 + spt, slots);
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int64_t mine = 0;
-    int units = 0, r = 0;
-    int64_t t = 0;
-    for (int64_t s = s0; s < s1; ++s) {
-        units = slot_units(a, R, s, r, t);
-        mine += (int64_t)units * a.c.Hkv;
-    }
-    int64_t x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) base[warp + 1] = x;
-    if (threadIdx.x == 0) base[0] = 0;
-    __syncthreads();
-    if (threadIdx.x == 0)
-        for (int i = 0; i < T / 32; ++i) base[i + 1] += base[i];
-    __syncthreads();
-    const int64_t total = base[T / 32];
-    const int64_t from = base[warp] + x - mine;   // first unit of this thread's slots
-    per = max((int64_t)min_units, (total + gridDim.x - 1) / gridDim.x);
-    begin = blockIdx.x * per;
-    end = min(begin + per, total);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && p.per) *p.per = per;
-    if (begin >= end) {
-        if (threadIdx.x == 0 && p.first) p.first[blockIdx.x] = Cursor{0, 0, 0, 0, 0};
-        return false;
-    }
-    if (from <= begin && begin < from + mine) {
-        int64_t left = begin - from;
-        if (spt > 1)                              // (one slot: it is at hand)
-            for (int64_t s = s0; s < s1; ++s) {
-                units = slot_units(a, R, s, r, t);
-                if (left < (int64_t)units * a.c.Hkv) break;
-                left -= (int64_t)units * a.c.Hkv;
-            }
-        units = max(units, 1);
-        first.r = r;
-        first.t = (int)t;
-        first.g = min((int)(left / units), a.c.Hkv - 1);
-        first.u = (int)(left % units);
-        first.units = units;
-        if (p.first) p.first[blockIdx.x] = first;
-    }
-    __syncthreads();
-    cur = first;
+    if (t < 0 || t >= row_tiles(a, s, R)) return false;
+    k = tile_keys(a, s, r, R, (int)t);
     return true;
 }
 
 // The segment after cur; cur.r = n_rows behind the last one.
-__device__ __forceinline__ void plan_next(const AttendArgs &a, int R, Cursor &cur) {
+template <typename U>
+__device__ __forceinline__ void plan_next(const AttendArgs &a, const U &w, int R, Cursor &cur) {
     cur.u = 0;
     if (++cur.g < a.c.Hkv) return;
     cur.g = 0;
@@ -173,9 +133,107 @@ __device__ __forceinline__ void plan_next(const AttendArgs &a, int R, Cursor &cu
     for (; cur.r < a.c.n_rows; ++cur.r, cur.t = 0) {
         const RowSpan s = row_span(a.c, cur.r, a.max_q);
         if (cur.t >= row_tiles(a, s, R)) continue;
-        cur.units = range_units(a, tile_keys(a, s, cur.r, R, cur.t));
+        cur.units = range_units(a, w, tile_keys(a, s, cur.r, R, cur.t));
         return;
     }
+}
+
+// Shared memory of plan_begin.
+template <int T>
+struct PlanSmem {
+    int64_t base[T / 32 + 1];
+    int64_t edge[2];
+    Cursor first;
+};
+
+// Exclusive sum over the block's threads; the sum of all is sm.base[T / 32].
+template <int T>
+__device__ __forceinline__ int64_t plan_scan(PlanSmem<T> &sm, int64_t v) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sm.base[warp + 1] = x;
+    if (threadIdx.x == 0) sm.base[0] = 0;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int i = 0; i < T / 32; ++i) sm.base[i + 1] += sm.base[i];
+    __syncthreads();
+    return sm.base[warp] + x - v;
+}
+
+// Every thread of the block gets the block's first cursor and [begin, end)
+// (false: no work).  T = threads of the block; w: shared memory where it is Parts.
+template <int T, typename U>
+__device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_units, PlanSmem<T> &sm,
+                                           const PlanOut &p, U &w, Cursor &cur, int64_t &begin, int64_t &end) {
+    const int64_t slots = tile_slots(a, R), spt = (slots + T - 1) / T;
+    const int64_t s0 = min(threadIdx.x * spt, slots), s1 = min(s0 + spt, slots);
+    int units = 0, r = 0;
+    int64_t t = 0;
+    KeyRange k{0, 0};
+    if constexpr (U::kParts) {   // chunks and segments in all
+        int64_t both = 0;
+        if (!a.whole)
+            for (int64_t s = s0; s < s1; ++s)
+                if (slot_keys(a, R, s, r, t, k)) both += ((int64_t)range_chunks(k) << 24) + 1;
+        plan_scan<T>(sm, both);
+        const int64_t segs = (sm.base[T / 32] & 0xffffff) * a.c.Hkv, chunks = (sm.base[T / 32] >> 24) * a.c.Hkv;
+        const bool few = segs > 0 && segs * 2 <= gridDim.x && chunks < 0x7fffffff;
+        if (threadIdx.x == 0) {
+            w.parts = few ? (int)(gridDim.x - segs) : 0;
+            w.chunks = few ? max((int)chunks, 1) : 1;
+        }
+        __syncthreads();
+        if (few) min_units = 1;
+    }
+    int64_t mine = 0;
+    for (int64_t s = s0; s < s1; ++s) {
+        units = 0;
+        if (slot_keys(a, R, s, r, t, k)) units = range_units(a, w, k);
+        mine += (int64_t)units * a.c.Hkv;
+    }
+    const int64_t from = plan_scan<T>(sm, mine);     // first unit of this thread's slots
+    const int64_t total = sm.base[T / 32];
+    const int64_t per = max((int64_t)min_units, (total + gridDim.x - 1) / gridDim.x);
+    // the block's two edges, each found by the thread whose slots hold it
+#pragma unroll 1
+    for (int e = 1; e >= 0; --e) {
+        const int64_t edge = min((blockIdx.x + e) * per, total);
+        if (edge == total && threadIdx.x == 0) sm.edge[e] = total;
+        if (from > edge || edge >= from + mine) continue;
+        int64_t left = edge - from;
+        if (spt > 1)                              // (one slot: it is at hand)
+            for (int64_t s = s0; s < s1; ++s) {
+                units = 0;
+                if (slot_keys(a, R, s, r, t, k)) units = range_units(a, w, k);
+                if (left < (int64_t)units * a.c.Hkv) break;
+                left -= (int64_t)units * a.c.Hkv;
+            }
+        units = max(units, 1);
+        int u = (int)(left % units);
+        if (!U::kParts || w.parts == 0) {
+            if (u > 0 && u - a.lead < a.lead) u = 0;
+            if (u > 0 && units - u < a.lead) u = units;
+        }
+        sm.edge[e] = edge - left % units + u;
+        sm.first = Cursor{r, (int)t, min((int)(left / units), a.c.Hkv - 1), u, units};
+    }
+    __syncthreads();
+    begin = sm.edge[0];
+    end = sm.edge[1];
+    if (begin < end) {
+        cur = sm.first;
+        if (cur.u == cur.units) plan_next(a, w, R, cur);
+    } else {
+        cur = Cursor{0, 0, 0, 0, 0};
+    }
+    if (threadIdx.x == 0 && p.first) p.first[blockIdx.x] = cur;
+    return begin < end;
 }
 
 // Query i of row span s at position pos sees [lo, hi).
@@ -192,12 +250,19 @@ __device__ __forceinline__ KeyRange query_keys(const AttendArgs &a, const RowSpa
 }
 
 // The keys of units [cur.u, u1) of segment cur (hi <= lo: none).
-__device__ __forceinline__ KeyRange segment_keys(const AttendArgs &a, const RowSpan &s, const Cursor &cur, int u1,
-                                                 int R) {
+template <typename U>
+__device__ __forceinline__ KeyRange segment_keys(const AttendArgs &a, const U &w, const RowSpan &s,
+                                                 const Cursor &cur, int u1, int R) {
     const KeyRange k = tile_keys(a, s, cur.r, R, cur.t);
     if (a.whole) return k;
-    const int unit0 = k.lo / kUnitKeys;
-    return KeyRange{max(k.lo, (unit0 + cur.u) * kUnitKeys), min(k.hi, (unit0 + u1) * kUnitKeys)};
+    const int c0 = k.lo / kUnitKeys;
+    int b = max(cur.u - a.lead, 0), e = max(u1 - a.lead, 0);        // chunks of the range
+    if (U::kParts && w.parts > 0) {
+        const int64_t n = range_chunks(k);
+        b = (int)(cur.u * n / cur.units);
+        e = (int)(u1 * n / cur.units);
+    }
+    return KeyRange{max(k.lo, (c0 + b) * kUnitKeys), min(k.hi, (c0 + e) * kUnitKeys)};
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {   // one MUFU op; tiny results flush to 0

@@ -163,7 +163,8 @@ xgr_status xgr_cache_store(const xgr_cache *cache, const xgr_cache_rows *rows, c
  * d_table_out int32 [n_out][max_pages] and d_len_out [n_out] must not overlap
  * the arrays read.  The cache's pages that `rows` holds are not changed, so a
  * step can be taken back by going on from `rows`. */
-xgr_status xgr_cache_fork_bytes(const xgr_cache *cache, int32_t n_out, size_t *bytes);
+xgr_status xgr_cache_fork_bytes(const xgr_cache *cache, int32_t n_rows, int32_t n_out,
+                                size_t *bytes);
 xgr_status xgr_cache_fork(const xgr_cache *cache, const xgr_cache_rows *rows, int32_t n_out,
                           const int32_t *d_parent, const int32_t *d_n_new, int32_t *d_table_out,
                           int32_t *d_len_out, void *d_ws, size_t ws_bytes, int32_t *d_status,

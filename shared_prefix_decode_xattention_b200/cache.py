@@ -203,7 +203,8 @@ class PagedCache:
         d_new = None if n_new is None else self._int32(fn, "n_new", n_new, (n_out,))
         d_table = self._int32(fn, "table_out", table_out, (n_out, rows.max_pages))
         d_len = self._int32(fn, "len_out", len_out, (n_out,))
-        need = self._bytes(("fork", n_out), lambda: xgr.xgr_cache_fork_bytes(self._c, n_out))
+        need = self._bytes(("fork", rows.n_rows, n_out),
+                           lambda: xgr.xgr_cache_fork_bytes(self._c, rows.n_rows, n_out))
         st = self._stream(stream)
         _, size, d_ws = self._workspace(fn, st, need)
         xgr.xgr_cache_fork(self._c, rows, n_out, d_parent, d_new, d_table, d_len, d_ws, size, self._d_status, st)

@@ -72,8 +72,10 @@ struct ForkArgs {
     int n_out;
     const int32_t *parent, *n_new;
     int32_t *table_out, *len_out;
-    uint32_t *used;             // [words] pages some out row holds
+    uint32_t *used, *full;      // [words] pages some out row holds, and holds as a full page
+    int32_t *sums;              // [16] the plan's CTAs' sums
     int32_t *lowest;            // [n_pages] lowest out row with the page as its partly filled last one
+    int32_t *owner;             // [n_rows] the child that marks a parent's pages
     int32_t *row_need;          // [n_out] pages handed out before the row
     int32_t *row_copy;          // [n_out] 1: the row's first new page takes a copy
     int32_t *free_list;         // [n_pages] free pages, ascending
@@ -83,8 +85,10 @@ struct ForkArgs {
 struct CompactArgs {
     CacheArgs c;
     int32_t *table_out, *n_used;
-    uint32_t *used;             // [words]
-    int32_t *prefix;            // [words + 1] pages held before the word
+    uint32_t *used;             // [words] pages that rows hold
+    int32_t *sums;              // [8] the plan's CTAs' sums
+    int32_t *below;             // [1] held pages below U
+    int32_t *prefix;            // [words] pages held before the word
     int32_t *hole;              // [n_pages] free slots below U, ascending
     int32_t *far;               // [n_pages] held pages from U on, ascending
 };

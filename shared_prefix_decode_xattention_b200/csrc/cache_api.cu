@@ -18,6 +18,8 @@ xgr_status check_cache(const xgr_cache *c, int *shift) {
     if (!c) return XGR_ERR_ARG;
     if (c->format != XGR_CACHE_E4M3 && c->format != XGR_CACHE_INT8) return XGR_ERR_ARG;
     if (c->n_pages < 1 || c->n_pages > kMaxPages || c->n_kv_heads < 1 || c->n_kv_heads > 1024) return XGR_ERR_SHAPE;
+    // (blocks of 16 keys of a head are counted in 32 bits)
+    if ((int64_t)c->n_pages * c->n_kv_heads * (c->page_size / 16) > 0x7fffffffll) return XGR_ERR_SHAPE;
     if (c->head_dim != 64 && c->head_dim != 128) return XGR_ERR_UNIMPLEMENTED;
     switch (c->page_size) {
         case 16: *shift = 4; break;
@@ -146,22 +148,24 @@ extern "C" xgr_status xgr_cache_store(const xgr_cache *cache, const xgr_cache_ro
 namespace {
 
 struct ForkWs {
-    size_t used, lowest, need, copy, list, n_free, total;
+    size_t used, full, lowest, owner, need, copy, list, sums, total;
 };
-ForkWs fork_ws(const xgr_cache *c, int32_t n_out) {
+ForkWs fork_ws(const xgr_cache *c, int32_t n_rows, int32_t n_out) {
     ForkWs w{};
     w.used = 0;
-    w.lowest = up(words_of(c) * 4);
-    w.need = w.lowest + up((size_t)c->n_pages * 4);
+    w.full = up(words_of(c) * 4);
+    w.lowest = w.full + up(words_of(c) * 4);
+    w.owner = w.lowest + up((size_t)c->n_pages * 4);
+    w.need = w.owner + up((size_t)n_rows * 4);
     w.copy = w.need + up((size_t)n_out * 4);
     w.list = w.copy + up((size_t)n_out * 4);
-    w.n_free = w.list + up((size_t)c->n_pages * 4);
-    w.total = w.n_free + kAlign;
+    w.sums = w.list + up((size_t)c->n_pages * 4);       // 16 sums, the number of free pages
+    w.total = w.sums + kAlign;
     return w;
 }
 
 struct CompactWs {
-    size_t used, prefix, hole, far, total;
+    size_t used, prefix, hole, far, sums, total;
 };
 CompactWs compact_ws(const xgr_cache *c) {
     CompactWs w{};
@@ -169,19 +173,21 @@ CompactWs compact_ws(const xgr_cache *c) {
     w.prefix = up(words_of(c) * 4);
     w.hole = w.prefix + up(words_of(c) * 4);
     w.far = w.hole + up((size_t)c->n_pages * 4);
-    w.total = w.far + up((size_t)c->n_pages * 4);
+    w.sums = w.far + up((size_t)c->n_pages * 4);        // 8 sums, the held pages below U
+    w.total = w.sums + kAlign;
     return w;
 }
 
 }  // namespace
 
-extern "C" xgr_status xgr_cache_fork_bytes(const xgr_cache *cache, int32_t n_out, size_t *bytes) {
+extern "C" xgr_status xgr_cache_fork_bytes(const xgr_cache *cache, int32_t n_rows, int32_t n_out,
+                                           size_t *bytes) {
     int shift = 0;
     const xgr_status st = check_cache(cache, &shift);
     if (st != XGR_OK) return st;
     if (!bytes) return XGR_ERR_ARG;
-    if (n_out < 0) return XGR_ERR_SHAPE;
-    *bytes = fork_ws(cache, n_out).total;
+    if (n_rows < 0 || n_out < 0) return XGR_ERR_SHAPE;
+    *bytes = fork_ws(cache, n_rows, n_out).total;
     return XGR_OK;
 }
 
@@ -207,7 +213,7 @@ extern "C" xgr_status xgr_cache_fork(const xgr_cache *cache, const xgr_cache_row
     for (int o = 0; o < 2; ++o)
         for (int i = 0; i < 4; ++i)
             if (in_n[i] && overlaps(out[o], out_n[o], in[i], in_n[i])) return XGR_ERR_ARG;
-    const ForkWs w = fork_ws(cache, n_out);
+    const ForkWs w = fork_ws(cache, rows->n_rows, n_out);
     if (ws_bytes < w.total) return XGR_ERR_CAPACITY;
     uint8_t *ws = static_cast<uint8_t *>(d_ws);
     a.n_out = n_out;
@@ -216,11 +222,14 @@ extern "C" xgr_status xgr_cache_fork(const xgr_cache *cache, const xgr_cache_row
     a.table_out = d_table_out;
     a.len_out = d_len_out;
     a.used = reinterpret_cast<uint32_t *>(ws + w.used);
+    a.full = reinterpret_cast<uint32_t *>(ws + w.full);
     a.lowest = reinterpret_cast<int32_t *>(ws + w.lowest);
+    a.owner = reinterpret_cast<int32_t *>(ws + w.owner);
     a.row_need = reinterpret_cast<int32_t *>(ws + w.need);
     a.row_copy = reinterpret_cast<int32_t *>(ws + w.copy);
     a.free_list = reinterpret_cast<int32_t *>(ws + w.list);
-    a.n_free = reinterpret_cast<int32_t *>(ws + w.n_free);
+    a.sums = reinterpret_cast<int32_t *>(ws + w.sums);
+    a.n_free = a.sums + 32;
     return launch_cache_fork(a, (cudaStream_t)stream) == cudaSuccess ? XGR_OK : XGR_ERR_CUDA;
 }
 
@@ -253,5 +262,7 @@ extern "C" xgr_status xgr_cache_compact(const xgr_cache *cache, const xgr_cache_
     a.prefix = reinterpret_cast<int32_t *>(ws + w.prefix);
     a.hole = reinterpret_cast<int32_t *>(ws + w.hole);
     a.far = reinterpret_cast<int32_t *>(ws + w.far);
+    a.sums = reinterpret_cast<int32_t *>(ws + w.sums);
+    a.below = a.sums + 32;
     return launch_cache_compact(a, (cudaStream_t)stream) == cudaSuccess ? XGR_OK : XGR_ERR_CUDA;
 }

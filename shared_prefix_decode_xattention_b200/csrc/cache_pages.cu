@@ -9,20 +9,32 @@
 // result is a function of the tables alone, the calls can be captured and
 // replayed, and a page cannot be freed twice.
 //
-// Both are bound by the copies of whole pages (each page's K and V are two
-// contiguous blocks of Hkv * page * D bytes); small calls by their four
-// dependent launches, which overlap by programmatic launch.
+// Each call is two kernels.  The plan runs on one cluster of eight CTAs, whose
+// hardware barrier separates its phases (clear, mark, count and place), so a
+// small call costs two launches instead of four; every CTA marks pages in a
+// bitset of its own in shared memory first (the beams of a request all hold
+// its prompt's pages, and that many atomics on one word took 120 us for 8192
+// rows of 129 pages).  The second kernel is bound by the copies of whole pages:
+// each page's K and V are two contiguous blocks of Hkv * page * D bytes.
 #include "cache.cuh"
 
 namespace xgr {
 
 namespace {
 
-constexpr int kScanThreads = 1024;   // the scan: one word of the bitset a thread, 32768 pages a block
+constexpr int kPlanCtas = 8;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlan = kPlanCtas * kPlanThreads;
+constexpr int kSmemWords = 24576;       // two bitsets of up to 786432 pages in shared memory; above, in global memory
 constexpr int kCopyThreads = 256;
 constexpr int64_t kPartBytes = 32768;   // bytes of one block's share of a page copy
 
-// Exclusive block scan of one int per thread (block of kScanThreads); *total gets the sum.
+// Every thread of the cluster gets here before any goes on, and sees what the others wrote before.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// Exclusive block scan of one int per thread (block of kPlanThreads); *total gets the sum.
 __device__ __forceinline__ int block_scan(int v, int *total) {
     __shared__ int part[33];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -51,13 +63,56 @@ __device__ __forceinline__ int block_scan(int v, int *total) {
     return part[warp] + x - v;
 }
 
-// words before `w` of a bitset: their set bits (every thread of the block gets the sum)
-__device__ __forceinline__ int bits_before(const uint32_t *bits, int w) {
-    int n = 0;
-    for (int i = threadIdx.x; i < w; i += kScanThreads) n += __popc(bits[i]);
-    int total;
-    block_scan(n, &total);
-    return total;
+// [b, e) of n things for this CTA, and of those for this thread (contiguous)
+__device__ __forceinline__ void my_share(int n, int &b, int &e) {
+    const int per = (n + kPlan - 1) / kPlan;
+    b = min((int)(blockIdx.x * kPlanThreads + threadIdx.x) * per, n);
+    e = min(b + per, n);
+}
+
+__device__ __forceinline__ bool page_ok(const CacheArgs &c, int id) { return id >= 0 && id < c.n_pages; }
+
+// A bitset that marks go to: this CTA's own in shared memory, or the one in global memory.
+__device__ __forceinline__ void mark(uint32_t *bits, int id) {
+    const uint32_t bit = 1u << (id & 31);
+    volatile uint32_t *w = bits + (id >> 5);
+    if (!(*w & bit)) atomicOr(bits + (id >> 5), bit);
+}
+
+// A warp marks the pages of a line's first `held` entries in `used`, and of its
+// first `full` ones in `whole`.  Eight entries a lane are read before the first
+// is marked: the marks' atomics would hold back every later read, and a line
+// would take a round trip per 32 entries.
+__device__ __forceinline__ void mark_line(const CacheArgs &c, const int32_t *line, int held, int full,
+                                          uint32_t *used, uint32_t *whole) {
+    const int lane = threadIdx.x % 32;
+    for (int i0 = lane; i0 < held; i0 += 256) {
+        int id[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) id[k] = i0 + 32 * k < held ? line[i0 + 32 * k] : 0x7fffffff;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (i0 + 32 * k >= held) break;
+            if (!page_ok(c, id[k])) {
+                set_status(c.status, XGR_DEV_INDEX);
+                continue;
+            }
+            mark(used, id[k]);
+            if (i0 + 32 * k < full) mark(whole, id[k]);
+        }
+    }
+}
+
+// Adds this CTA's marks to the bitset in global memory.
+__device__ __forceinline__ void flush_marks(uint32_t *to, const uint32_t *from, int words) {
+    for (int w = threadIdx.x; w < words; w += kPlanThreads)
+        if (from[w]) atomicOr(to + w, from[w]);
+}
+
+// the bits of word w that stand for pages
+__device__ __forceinline__ uint32_t word_mask(const CacheArgs &c, int w) {
+    const int n = c.n_pages - w * 32;
+    return n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
 // An out row of a fork: its parent's line and what it keeps of it.
@@ -86,95 +141,105 @@ __device__ __forceinline__ Child child_of(const ForkArgs &a, int r) {
     return c;
 }
 
-__device__ __forceinline__ bool page_ok(const CacheArgs &c, int id) { return id >= 0 && id < c.n_pages; }
-
 // ---------------------------------------------------------------- fork
 
-__global__ void __launch_bounds__(256) fork_clear_kernel(ForkArgs a, int words) {
+// Out row r's pages beyond its parent's, and whether the first takes a copy.
+__device__ __forceinline__ int row_need(const ForkArgs &a, int r, int &copy) {
+    const Child c = child_of(a, r);
+    copy = 0;
+    if (c.held > c.full) {
+        const int id = c.line[c.full];
+        copy = page_ok(a.c, id) && ((a.full[id >> 5] >> (id & 31) & 1) || a.lowest[id] != r);
+    }
+    int more = a.n_new && c.line ? a.n_new[r] : 0;
+    if (more < 0) {
+        set_status(a.c.status, XGR_DEV_INDEX);
+        more = 0;
+    }
+    const int64_t grown = min((int64_t)c.len + more, (int64_t)a.c.max_pages << a.c.page_shift);
+    return (int)((grown + a.c.page - 1) >> a.c.page_shift) - c.held + copy;
+}
+
+// Phases: clear; mark the pages that out rows hold; then the pages each row
+// needs and the free pages, each as its share's sum, and after one more barrier
+// in place.
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a, int words) {
+    extern __shared__ uint32_t own[];
     griddep_wait();
     griddep_launch_dependents();
-    const int stride = gridDim.x * 256;
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < words; i += stride) a.used[i] = 0;
-    // `lowest` is read at the rows' partly filled pages only
-    for (int r = blockIdx.x * 256 + threadIdx.x; r < a.n_out; r += stride) {
+    const bool in_smem = words <= kSmemWords;
+    const int tid = blockIdx.x * kPlanThreads + threadIdx.x, lane = threadIdx.x % 32;
+    for (int i = tid; i < words; i += kPlan) a.used[i] = a.full[i] = 0;
+    if (in_smem)
+        for (int i = threadIdx.x; i < 2 * words; i += kPlanThreads) own[i] = 0;
+    for (int r = tid; r < a.n_out; r += kPlan) {     // `lowest` is read at partly filled pages only
         const Child c = child_of(a, r);
         if (c.held > c.full) {
             const int id = c.line[c.full];
             if (page_ok(a.c, id)) a.lowest[id] = 0x7fffffff;
         }
+        if (c.line) a.owner[a.parent[r]] = r;        // of several children any one: it marks the parent's pages for all
     }
-}
-
-// A warp per out row marks the row's pages as used.  A prompt's pages are
-// marked by every beam that shares it: a plain load first keeps all but the
-// first few of the atomics away (a stale value only costs one more).
-__global__ void __launch_bounds__(256) fork_mark_kernel(ForkArgs a) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int lane = threadIdx.x % 32;
-    for (int r = blockIdx.x * 8 + threadIdx.x / 32; r < a.n_out; r += gridDim.x * 8) {
-        const Child c = child_of(a, r);
-        for (int i = lane; i < c.held; i += 32) {
-            const int id = c.line[i];
-            if (!page_ok(a.c, id)) {
-                set_status(a.c.status, XGR_DEV_INDEX);
-                continue;
+    cluster_sync();
+    uint32_t *used = in_smem ? own : a.used, *full = in_smem ? own + words : a.full;
+    // a warp takes up to 32 rows at a time: their parents and lengths are read at once, then their lines
+    const int rows = min(32, (a.n_out + kPlan / 32 - 1) / (kPlan / 32));
+    for (int r0 = tid / 32 * rows; r0 < a.n_out; r0 += kPlan / 32 * rows) {
+        Child c{nullptr, 0, 0, 0};
+        if (lane < rows && r0 + lane < a.n_out) {
+            const int r = r0 + lane;
+            c = child_of(a, r);
+            if (c.held > c.full) {
+                const int id = c.line[c.full];
+                if (page_ok(a.c, id)) atomicMin(a.lowest + id, r);
             }
-            const uint32_t bit = 1u << (id & 31);
-            if (!(__ldcg(a.used + (id >> 5)) & bit)) atomicOr(a.used + (id >> 5), bit);
-            const int mine = i < c.full ? -1 : r;   // -1: a full page of some row, nobody's to write
-            if (__ldcg(a.lowest + id) > mine) atomicMin(a.lowest + id, mine);
+            if (c.line && a.owner[a.parent[r]] != r) c.held = 0;
+        }
+        for (int j = 0; j < rows; ++j) {
+            const int32_t *line = reinterpret_cast<const int32_t *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(c.line), j));
+            const int held = __shfl_sync(0xffffffffu, c.held, j);
+            mark_line(a.c, line, held, __shfl_sync(0xffffffffu, c.full, j), used, full);
+            __syncwarp();
         }
     }
-}
-
-// Block 0: pages each out row needs, as a prefix over the rows.  Blocks 1..:
-// the free pages in ascending order (each block its 32768 pages; the free ones
-// before them are counted from the bitset again, so no block waits).
-__global__ void __launch_bounds__(kScanThreads) fork_scan_kernel(ForkArgs a, int words) {
-    griddep_wait();
-    griddep_launch_dependents();
-    if (blockIdx.x == 0) {
-        int base = 0;
-        for (int r0 = 0; r0 < a.n_out; r0 += kScanThreads) {
-            const int r = r0 + threadIdx.x;
-            int need = 0, copy = 0;
-            if (r < a.n_out) {
-                const Child c = child_of(a, r);
-                if (c.held > c.full) {
-                    const int id = c.line[c.full];
-                    copy = page_ok(a.c, id) && a.lowest[id] != r;
-                }
-                int more = a.n_new ? a.n_new[r] : 0;
-                if (!c.line) more = 0;
-                if (more < 0) {
-                    set_status(a.c.status, XGR_DEV_INDEX);
-                    more = 0;
-                }
-                const int64_t grown = std::min((int64_t)c.len + more, (int64_t)a.c.max_pages << a.c.page_shift);
-                const int want = (int)((grown + a.c.page - 1) >> a.c.page_shift);
-                need = want - c.held + copy;
-                a.row_copy[r] = copy;
-            }
-            int total;
-            const int before = block_scan(need, &total);
-            if (r < a.n_out) a.row_need[r] = base + before;
-            base += total;
-        }
-        return;
+    if (in_smem) {
+        __syncthreads();
+        flush_marks(a.used, own, words);
+        flush_marks(a.full, own + words, words);
     }
-    const int w0 = (blockIdx.x - 1) * kScanThreads;
-    const int free_before = w0 * 32 - bits_before(a.used, w0);
-    const int w = w0 + threadIdx.x;
-    uint32_t bits = 0;
-    if (w < words) {
-        bits = ~a.used[w];
-        if ((w + 1) * 32 > a.c.n_pages) bits &= (1u << (a.c.n_pages & 31)) - 1u;   // (n_pages not a multiple of 32)
+    cluster_sync();
+    int r0, r1, w0, w1, need = 0, copy, free = 0;
+    my_share(a.n_out, r0, r1);
+    my_share(words, w0, w1);
+#pragma unroll 4
+    for (int r = r0; r < r1; ++r) {
+        const int n = row_need(a, r, copy);
+        a.row_copy[r] = copy;
+        a.row_need[r] = n;
+        need += n;
     }
-    int total;
-    int at = free_before + block_scan(__popc(bits), &total);
-    for (; bits; bits &= bits - 1) a.free_list[at++] = w * 32 + __ffs(bits) - 1;
-    if (w0 + kScanThreads >= words && threadIdx.x == 0) *a.n_free = free_before + total;
+    for (int w = w0; w < w1; ++w) free += __popc(~a.used[w] & word_mask(a.c, w));
+    int all_need, all_free;
+    need = block_scan(need, &all_need);
+    free = block_scan(free, &all_free);
+    if (threadIdx.x == 0) {
+        a.sums[blockIdx.x] = all_need;
+        a.sums[kPlanCtas + blockIdx.x] = all_free;
+    }
+    cluster_sync();
+    for (int i = 0; i < (int)blockIdx.x; ++i) {
+        need += a.sums[i];
+        free += a.sums[kPlanCtas + i];
+    }
+    for (int r = r0; r < r1; ++r) {
+        const int n = a.row_need[r];
+        a.row_need[r] = need;
+        need += n;
+    }
+    for (int w = w0; w < w1; ++w)
+        for (uint32_t b = ~a.used[w] & word_mask(a.c, w); b; b &= b - 1) a.free_list[free++] = w * 32 + __ffs(b) - 1;
+    if (tid == kPlan - 1) *a.n_free = free;          // (the last share ends at the last word)
 }
 
 // 16-byte copy of `bytes` (a multiple of 16) by the block, eight loads in flight a thread
@@ -257,12 +322,6 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(ForkArgs a, in
 
 // ---------------------------------------------------------------- compact
 
-__global__ void __launch_bounds__(256) compact_clear_kernel(CompactArgs a, int words) {
-    griddep_wait();
-    griddep_launch_dependents();
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < words; i += gridDim.x * 256) a.used[i] = 0;
-}
-
 __device__ __forceinline__ int pages_of(const CacheArgs &c, int r) {
     const int len = c.len[r];
     if (len < 0 || len > (int64_t)c.max_pages * c.page) {
@@ -272,51 +331,62 @@ __device__ __forceinline__ int pages_of(const CacheArgs &c, int r) {
     return (int)(((int64_t)len + c.page - 1) >> c.page_shift);
 }
 
-__global__ void __launch_bounds__(256) compact_mark_kernel(CompactArgs a) {
+// Phases: clear; mark the pages that rows hold; their sums; then held pages
+// before each word, the free slots below U and the held pages from U on, both
+// ascending.
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactArgs a, int words) {
+    extern __shared__ uint32_t own[];
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x % 32;
-    for (int r = blockIdx.x * 8 + threadIdx.x / 32; r < a.c.n_rows; r += gridDim.x * 8) {
-        const int held = pages_of(a.c, r);
-        const int32_t *line = a.c.table + (int64_t)r * a.c.max_pages;
-        for (int i = lane; i < held; i += 32) {
-            const int id = line[i];
-            if (!page_ok(a.c, id)) {
-                set_status(a.c.status, XGR_DEV_INDEX);
-                continue;
-            }
-            const uint32_t bit = 1u << (id & 31);
-            if (!(__ldcg(a.used + (id >> 5)) & bit)) atomicOr(a.used + (id >> 5), bit);
+    const bool in_smem = words <= kSmemWords;
+    const int tid = blockIdx.x * kPlanThreads + threadIdx.x;
+    for (int i = tid; i < words; i += kPlan) a.used[i] = 0;
+    if (in_smem)
+        for (int i = threadIdx.x; i < words; i += kPlanThreads) own[i] = 0;
+    cluster_sync();
+    uint32_t *used = in_smem ? own : a.used;
+    for (int r = tid / 32; r < a.c.n_rows; r += kPlan / 32) {
+        mark_line(a.c, a.c.table + (int64_t)r * a.c.max_pages, pages_of(a.c, r), 0, used, used);
+    }
+    if (in_smem) {
+        __syncthreads();
+        flush_marks(a.used, own, words);
+    }
+    cluster_sync();
+    int w0, w1, held = 0, all;
+    my_share(words, w0, w1);
+    for (int w = w0; w < w1; ++w) held += __popc(a.used[w]);
+    held = block_scan(held, &all);
+    if (threadIdx.x == 0) a.sums[blockIdx.x] = all;
+    cluster_sync();
+    int U = 0;
+    for (int i = 0; i < kPlanCtas; ++i) {
+        if (i < (int)blockIdx.x) held += a.sums[i];
+        U += a.sums[i];
+    }
+    for (int w = w0; w < w1; ++w) {
+        a.prefix[w] = held;
+        const uint32_t bits = a.used[w];
+        if (U >= w * 32 && U < w * 32 + 32) *a.below = held + __popc(bits & ((1u << (U & 31)) - 1u));
+        held += __popc(bits);
+    }
+    if (tid == 0) {
+        *a.n_used = U;
+        if (U >= words * 32) *a.below = U;           // (every page is held)
+    }
+    cluster_sync();
+    const int below = *a.below;                      // held pages below U: the far pages' ranks start there
+    for (int w = w0; w < w1; ++w) {
+        const uint32_t bits = a.used[w];
+        const int before = a.prefix[w];
+        for (uint32_t b = bits; b; b &= b - 1) {
+            const int j = __ffs(b) - 1, id = w * 32 + j;
+            if (id >= U) a.far[before + __popc(bits & ((1u << j) - 1u)) - below] = id;
         }
-    }
-}
-
-// Each block its 32768 pages: held pages before each word, the free slots below
-// U and the held pages from U on, both ascending.
-__global__ void __launch_bounds__(kScanThreads) compact_scan_kernel(CompactArgs a, int words) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int U = bits_before(a.used, words);
-    const int w0 = blockIdx.x * kScanThreads;
-    const int before = bits_before(a.used, w0);
-    const int w = w0 + threadIdx.x;
-    const uint32_t bits = w < words ? a.used[w] : 0u;
-    int total;
-    const int mine = before + block_scan(__popc(bits), &total);   // held pages before word w
-    if (w < words) a.prefix[w] = mine;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_used = U;
-    // held pages below U: the far pages' ranks start there
-    const int uw = U >> 5;
-    int below = bits_before(a.used, uw);
-    if (uw < words) below += __popc(a.used[uw] & ((1u << (U & 31)) - 1u));
-    if (w >= words) return;
-    for (uint32_t b = bits; b; b &= b - 1) {
-        const int j = __ffs(b) - 1, id = w * 32 + j;
-        if (id >= U) a.far[mine + __popc(bits & ((1u << j) - 1u)) - below] = id;
-    }
-    for (uint32_t b = ~bits; b; b &= b - 1) {
-        const int j = __ffs(b) - 1, id = w * 32 + j;
-        if (id < U) a.hole[id - mine - __popc(bits & ((1u << j) - 1u))] = id;
+        for (uint32_t b = ~bits; b; b &= b - 1) {
+            const int j = __ffs(b) - 1, id = w * 32 + j;
+            if (id < U) a.hole[id - before - __popc(bits & ((1u << j) - 1u))] = id;
+        }
     }
 }
 
@@ -327,7 +397,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(CompactArgs
     auto before = [&](int id) {   // held pages before page id
         return a.prefix[id >> 5] + __popc(a.used[id >> 5] & ((1u << (id & 31)) - 1u));
     };
-    const int below = U < a.c.n_pages ? before(U) : U;
+    const int below = *a.below;
     const int64_t moves = (int64_t)(U - below) * parts;
     for (int64_t m = blockIdx.x; m < moves; m += gridDim.x) {
         const int k = (int)(m / parts);
@@ -353,31 +423,49 @@ int copy_parts(const CacheArgs &c) {
 
 }  // namespace
 
+// one cluster of kPlanCtas CTAs, as a programmatic dependent of the kernel before
+template <typename Args>
+static cudaError_t launch_plan(void (*kernel)(Args, int), const Args &a, int words, int sets, cudaStream_t s) {
+    static bool ready[kMaxDevices] = {};   // (one instance a kernel: their argument types differ)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sets * kSmemWords * 4);
+        if (e != cudaSuccess) return e;
+        ready[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kPlanCtas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = words <= kSmemWords ? (size_t)sets * words * 4 : 0;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kPlanCtas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a, words);
+}
+
 cudaError_t launch_cache_fork(const ForkArgs &a, cudaStream_t s) {
-    const int words = (a.c.n_pages + 31) / 32;
-    const int warps = std::min((a.n_out + 7) / 8, kSms * 8);
-    const int clear = std::min((std::max(words, a.n_out) + 255) / 256, kSms * 4);
-    cudaError_t e = launch_pdl(fork_clear_kernel, dim3(clear), dim3(256), 0, s, a, words);
-    if (e == cudaSuccess) e = launch_pdl(fork_mark_kernel, dim3(warps), dim3(256), 0, s, a);
-    const int blocks = 1 + (words + kScanThreads - 1) / kScanThreads;
-    if (e == cudaSuccess) e = launch_pdl(fork_scan_kernel, dim3(blocks), dim3(kScanThreads), 0, s, a, words);
+    const cudaError_t e = launch_plan(fork_plan_kernel, a, (a.c.n_pages + 31) / 32, 2, s);
+    if (e != cudaSuccess) return e;
     const int parts = copy_parts(a.c);
-    if (e == cudaSuccess)
-        e = launch_pdl(fork_apply_kernel, dim3(a.n_out * parts), dim3(kCopyThreads), 0, s, a, parts);
-    return e;
+    return launch_pdl(fork_apply_kernel, dim3(a.n_out * parts), dim3(kCopyThreads), 0, s, a, parts);
 }
 
 cudaError_t launch_cache_compact(const CompactArgs &a, cudaStream_t s) {
-    const int words = (a.c.n_pages + 31) / 32;
-    cudaError_t e = launch_pdl(compact_clear_kernel, dim3(std::min((words + 255) / 256, kSms)), dim3(256), 0, s, a, words);
-    if (e == cudaSuccess)
-        e = launch_pdl(compact_mark_kernel, dim3(std::min((a.c.n_rows + 7) / 8, kSms * 8)), dim3(256), 0, s, a);
-    const int blocks = (words + kScanThreads - 1) / kScanThreads;
-    if (e == cudaSuccess)
-        e = launch_pdl(compact_scan_kernel, dim3(blocks), dim3(kScanThreads), 0, s, a, words);
-    if (e == cudaSuccess)
-        e = launch_pdl(compact_apply_kernel, dim3(kSms * 8), dim3(kCopyThreads), 0, s, a, copy_parts(a.c));
-    return e;
+    const cudaError_t e = launch_plan(compact_plan_kernel, a, (a.c.n_pages + 31) / 32, 1, s);
+    if (e != cudaSuccess) return e;
+    const int parts = copy_parts(a.c);
+    const int64_t most = std::max<int64_t>(a.c.n_rows, (int64_t)a.c.n_pages / 2 * parts);   // (moves fill free slots)
+    return launch_pdl(compact_apply_kernel, dim3((unsigned)std::min<int64_t>(kSms * 8, std::max<int64_t>(most, 1))),
+                      dim3(kCopyThreads), 0, s, a, parts);
 }
 
 }  // namespace xgr

@@ -192,7 +192,7 @@ def lib():
         "xgr_cache_attend": [PC, PR, P, i32, i32, i32, P, i64, ctypes.POINTER(xgr_attn_opts), P, P, P,
                              ctypes.c_size_t, P, P],
         "xgr_cache_store": [PC, PR, P, i32, i32, P, P, i64, P, P],
-        "xgr_cache_fork_bytes": [PC, i32, PZ],
+        "xgr_cache_fork_bytes": [PC, i32, i32, PZ],
         "xgr_cache_fork": [PC, PR, i32, P, P, P, P, P, ctypes.c_size_t, P, P],
         "xgr_cache_compact_bytes": [PC, PZ],
         "xgr_cache_compact": [PC, PR, P, P, P, ctypes.c_size_t, P, P],
@@ -421,10 +421,10 @@ def xgr_cache_store(cache: xgr_cache, rows: xgr_cache_rows, cu, n_tokens: int, m
         token_stride, _ptr(status), _stream(stream)))
 
 
-def xgr_cache_fork_bytes(cache: xgr_cache, n_out: int) -> int:
+def xgr_cache_fork_bytes(cache: xgr_cache, n_rows: int, n_out: int) -> int:
     n = ctypes.c_size_t(0)
     _check("xgr_cache_fork_bytes",
-           lib().xgr_cache_fork_bytes(ctypes.byref(cache), n_out, ctypes.byref(n)))
+           lib().xgr_cache_fork_bytes(ctypes.byref(cache), n_rows, n_out, ctypes.byref(n)))
     return n.value
 
 

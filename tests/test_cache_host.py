@@ -132,10 +132,10 @@ def test_nothing_to_do_is_ok(L):
 def test_workspace_sizes(L):
     c = cache()
     assert xgr.xgr_cache_attend_bytes(c, 16, 100, 100) % 256 == 0
-    assert xgr.xgr_cache_fork_bytes(c, 1000) > 2 * 4 * 100 and xgr.xgr_cache_compact_bytes(c) % 256 == 0
+    assert xgr.xgr_cache_fork_bytes(c, 1000, 1000) > 2 * 4 * 100 and xgr.xgr_cache_compact_bytes(c) % 256 == 0
     with pytest.raises(xgr.XgrError):
         xgr.xgr_cache_attend_bytes(c, 15, 100, 100)
     with pytest.raises(xgr.XgrError):
-        xgr.xgr_cache_fork_bytes(c, -1)
+        xgr.xgr_cache_fork_bytes(c, 10, -1)
     assert L.xgr_cache_compact_bytes(ctypes.byref(c), None) == xgr.XGR_ERR_ARG
     assert L.xgr_cache_compact_bytes(None, None) == xgr.XGR_ERR_ARG

@@ -487,10 +487,11 @@ def test_fork_is_exact(seed):
         table, lens = want_t, want_l
 
 
-def test_fork_many_pages_and_rows():
-    """More pages than one block of the scan takes (32768), more rows than it has threads."""
+@pytest.mark.parametrize("pages", [70001, 800003])
+def test_fork_many_pages_and_rows(pages):
+    """More rows and pages than one share of the plan; more pages than its bitsets in shared memory hold (786432)."""
     rng = np.random.default_rng(0)
-    pages, page, width = 70001, 16, 5
+    page, width = 16, 5
     cache = random_cache(rng, pages, 1, page, 64, "int8")
     n = 2500
     lens = rng.integers(0, 3 * page, n).astype(np.int32)

@@ -86,11 +86,11 @@ struct Seg {
     __device__ int chunk_of(int h, int i) const { return narrow ? 2 * i + h : i; }
 };
 
-__device__ __forceinline__ Seg segment(const AttendArgs &a, const Parts &w, const Cursor &cur, int64_t left) {
+__device__ __forceinline__ Seg segment(const AttendArgs &a, const Parts &w, const Cursor &cur, int left) {
     constexpr int R = 256;
     Seg s;
     s.row = row_span(a.c, cur.r, a.max_q);
-    s.u1 = (int)min((int64_t)cur.units, cur.u + left);
+    s.u1 = min(cur.units, cur.u + left);
     const KeyRange k = segment_keys(a, w, s.row, cur, s.u1, R);
     s.kb0 = k.lo & ~(kChunk - 1);
     s.ke = k.hi;
@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
     Parts &units = *reinterpret_cast<Parts *>(base + L::misc + 8);
     int64_t begin, end;
     if (!plan_begin<kThreads>(a, R, min_units, *reinterpret_cast<PlanSmem<kThreads> *>(base + L::raw), po, units, cur, begin, end)) return;   // (of the whole block)
+    const int share = (int)(end - begin);            // units of this CTA
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                      "r"(kTmemCols)
@@ -164,8 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         int cnt = 0;       // of them, this warpgroup's
         int nx = 0;        // narrow segments before
         bool ok = true;
-        for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
-            const Seg s = segment(a, units, cur, end - at);
+        for (int left = share; ok && left > 0 && cur.r < c.n_rows;) {
+            const Seg s = segment(a, units, cur, left);
             const int ia = cur.t * R + tr + (s.narrow ? 0 : 128 * h);
             const bool valid = ia < s.row.n * a.G;
             const int tok = valid ? ia / a.G : 0, head = cur.g * a.G + (valid ? ia % a.G : 0);
@@ -431,8 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 tc::fence_before();
                 if (fold) mbar_arrive(bar(B_XDONE));
             }
-            at += s.u1 - cur.u;
-            if (at < end) plan_next(a, units, R, cur);
+            left -= s.u1 - cur.u;
+            if (left > 0) plan_next(a, units, R, cur);
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------ codes to operands
@@ -447,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         const int key_in = (t / 32) * (32 / kCh) + kr;             // key of the pass
         int gc = 0;
         bool ok = true;
-        for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
-            const Seg s = segment(a, units, cur, end - at);
+        for (int left = share; ok && left > 0 && cur.r < c.n_rows;) {
+            const Seg s = segment(a, units, cur, left);
             const int32_t *line = c.table + (int64_t)cur.r * c.max_pages;
             // Lane g of every warp holds group g % 8 of a chunk: its page (-2: no keys, -1: no such page), and where its
             // 16 keys lie, in blocks of 16 keys (they are contiguous in a page and head).
@@ -542,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 ids = ids2;
             }
             gc += s.chunks;
-            at += s.u1 - cur.u;
-            if (at < end) plan_next(a, units, R, cur);
+            left -= s.u1 - cur.u;
+            if (left > 0) plan_next(a, units, R, cur);
         }
         cp_async_wait_all();
     } else {
@@ -552,11 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         if (warp == 12) {
             constexpr uint32_t idS = tc::idesc_f16(128, 128, false), idO = tc::idesc_f16(128, D, true);
             int gc = 0, cnt0 = 0, cnt1 = 0, nq0 = 0, nq1 = 0;
-            const uint64_t dq = tc::desc(sb + L::q, 16, 1024), dk = tc::desc(sb + L::k, 16, 1024);
-            const uint64_t dv = tc::desc(sb + L::v, L::kHalf, 1024);
+            // operands' descriptors: their low words are these, the high word is the same for all
+            const uint32_t dq = tc::desc_lo(sb + L::q, 16), dk = tc::desc_lo(sb + L::k, 16), dv = tc::desc_lo(sb + L::v, L::kHalf);
             bool ok = true;
-            for (int64_t at = begin; ok && at < end && cur.r < c.n_rows;) {
-                const Seg s = segment(a, units, cur, end - at);
+            for (int left = share; ok && left > 0 && cur.r < c.n_rows;) {
+                const Seg s = segment(a, units, cur, left);
                 if (lane == 0 && s.chunks > 0) {
                     const int n[2] = {s.tile_chunks(0), s.tile_chunks(1)};
                     const int cnt[2] = {cnt0, cnt1};
@@ -577,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                                 if (mbar_test(bar(B_PFULL + h), (cnt[h] + ip[h]) & 1) &&
                                     mbar_test(bar(B_VFULL + st), (gi >> 1) & 1)) {
                                     tc::fence_after();
-                                    const uint64_t v = dv + st * (L::kTile >> 4);
+                                    const uint32_t v = dv + st * (L::kTile >> 4);
 #pragma unroll
                                     for (int k = 0; k < 8; ++k)
-                                        tc::mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 8u * k, v + k * (2048 >> 4),
+                                        tc::mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 8u * k, tc::desc_of(v + k * (2048 >> 4)),
                                                    idO, (k > 0 || ip[h] > 0) ? 1u : 0u);
                                     tc::commit(bar(B_PVDONE + h));
                                     tc::commit(bar(B_VEMPTY + st));
@@ -594,12 +595,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                                 const int gi = gc + s.chunk_of(h, is[h]), st = gi & 1;
                                 if (mbar_test(bar(B_KFULL + st), (gi >> 1) & 1)) {
                                     tc::fence_after();
-                                    const uint64_t q = dq + (s.narrow ? 0 : h) * (L::kTile >> 4);
-                                    const uint64_t kk = dk + st * (L::kTile >> 4);
+                                    const uint32_t q = dq + (s.narrow ? 0 : h) * (L::kTile >> 4);
+                                    const uint32_t kk = dk + st * (L::kTile >> 4);
 #pragma unroll
                                     for (int k = 0; k < D / 16; ++k) {
                                         const uint32_t off = ((uint32_t)(k >> 2) * L::kHalf + (uint32_t)(k & 3) * 32u) >> 4;
-                                        tc::mma_ss(tmem + 128u * h, q + off, kk + off, idS, k > 0);
+                                        tc::mma_ss(tmem + 128u * h, tc::desc_of(q + off), tc::desc_of(kk + off), idS, k > 0);
                                     }
                                     tc::commit(bar(B_SFULL + h));
                                     tc::commit(bar(B_KEMPTY + st));
@@ -625,8 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 }
                 ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
                 gc += s.chunks;
-                at += s.u1 - cur.u;
-                if (at < end) plan_next(a, units, R, cur);
+                left -= s.u1 - cur.u;
+                if (left > 0) plan_next(a, units, R, cur);
             }
             if (lane == 0) {   // every product issued has completed before tensor memory is given back
                 tc::commit(bar(B_DONE));

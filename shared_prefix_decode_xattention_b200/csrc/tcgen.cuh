@@ -7,15 +7,16 @@
 namespace xgr {
 namespace tc {
 
-// Shared-memory matrix descriptor, 128-byte swizzle (sm_100 format: version 1).
-__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// Shared-memory matrix descriptor, 128-byte swizzle (sm_100 format: version 1),
+// 1024 bytes between groups of eight rows: its low word, which holds the
+// address and the leading offset, and all of it.  A step inside the operand
+// adds its bytes / 16 to the low word.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+    return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) & 0x3FFFu) << 16;
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+    constexpr uint32_t hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+    return (uint64_t)hi << 32 | lo;
 }
 
 // Instruction descriptor of kind::f16: fp16 A and B, fp32 accumulator.

@@ -15,17 +15,27 @@
 //   warps 0-7    two softmax warpgroups, a query row a thread: scores from
 //                tensor memory, cap, bias, mask, weights back over the scores'
 //                buffer as fp16, and at a segment's end the output;
-//   warps 8-11   the codes of each 128-key chunk, 16 bytes a copy from the pages
-//                one chunk ahead, converted and written as the
-//                128-byte-swizzled operands of K and V (rings of two);
-//   warp 12      issues the products: S_h = Q_h K^T, O_h += W_h V, whichever of
+//   warp 8       issues the products: S_h = Q_h K^T, O_h += W_h V, whichever of
 //                the two tiles is ready, so one tile's softmax runs beside the
-//                other's products.
+//                other's products;
+//   warps 9-15   the codes of each 128-key chunk, 16 bytes a copy from the pages
+//                one chunk ahead, converted and written as the
+//                128-byte-swizzled operands of K and V (rings of two).
 // A conversion serves 256 query rows.  With 128 rows or fewer (a "narrow"
 // segment) both warpgroups take the same rows and alternate chunks, and the
 // first one folds the second's result in at the end.
 // Registers: 512 threads start with 128 each; the softmax warpgroups take 192,
-// the conversion and the issuing group keep 64 (their sum is what the block has).
+// the other two keep 64 (their sum is what the block has).
+//
+// What bounds it: a tile's chain of softmax, W V and the next Q K^T, whose
+// scores may only be written once W V has read the weights over the old ones
+// (tensor memory is full: two S, two O of 128 columns); two tiles overlap their
+// chains.  Measured at 512 beams x 32 heads over 4096 keys, 16 requests (550
+// GFLOP; 1692 TFLOP/s of bf16 would take 325 us): 684 us, 805 TFLOP/s, 0.48 of the
+// measured bf16 rate; four conversion warps 696 us, three 870; weights through
+// shared memory instead, so that the next scores need not wait, 740 us (the
+// writes, and single operand buffers for want of room); the scores read in two
+// rolled passes 790 us; spills in the issuing warp (48 registers) 822 us.
 // Every wait is bounded (XGR_DEV_TIMEOUT and an unwound CTA, no hang).
 #include "cache_codes.cuh"
 #include "cache_plan.cuh"
@@ -36,7 +46,9 @@ namespace xgr {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kConvThreads = 128;
+constexpr int kConvWarps = 7;
+constexpr int kConvThreads = 32 * kConvWarps;
+constexpr int kIssueWarp = 8;
 constexpr int kChunk = 128;                    // keys of a chunk
 constexpr int kRing = 4;                       // chunks whose scales are at hand
 constexpr uint32_t kTmemCols = 512;            // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512)
@@ -142,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
     int64_t begin, end;
     if (!plan_begin<kThreads>(a, R, min_units, *reinterpret_cast<PlanSmem<kThreads> *>(base + L::raw), po, units, cur, begin, end)) return;   // (of the whole block)
     const int share = (int)(end - begin);            // units of this CTA
-    if (warp == 12) {
+    if (warp == kIssueWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                      "r"(kTmemCols)
                      : "memory");
@@ -435,17 +447,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             left -= s.u1 - cur.u;
             if (left > 0) plan_next(a, units, R, cur);
         }
-    } else if (warp < 12) {
+    } else if (warp > kIssueWarp) {
         // ------------------------------------------------------------ codes to operands
         tc::regs_down<64>();
-        const int t = tid - 256;
-        // lane -> (key, 16-byte chunk) of a group of 16 keys, so that eight lanes' 16-byte writes meet no bank twice
-        constexpr int kCh = D / 16;                                // chunks of a key
+        const int cw = warp - kIssueWarp - 1;
+        // A block is the 512 bytes (kKeys keys) that a warp copies or converts at a time; the warps take every third.
+        // lane -> (key, 16-byte chunk) so that eight lanes' 16-byte writes meet no bank twice
+        constexpr int kKeys = 512 / D, kBlocks = kChunk / kKeys, kTurns = (kBlocks + kConvWarps - 1) / kConvWarps;
         const int ck = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
         const int kr = D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
-        constexpr int kRows = 128 / kCh;                           // keys of one pass of the 128 threads
-        constexpr int kPass = kChunk / kRows;
-        const int key_in = (t / 32) * (32 / kCh) + kr;             // key of the pass
         int gc = 0;
         bool ok = true;
         for (int left = share; ok && left > 0 && cur.r < c.n_rows;) {
@@ -459,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 if (ch < s.chunks && key < s.ke) {
                     id = line[key >> c.page_shift];
                     if (id < 0 || id >= c.n_pages) {
-                        if (t == lane) set_status(c.status, XGR_DEV_INDEX);
+                        if (cw == 0) set_status(c.status, XGR_DEV_INDEX);
                         id = -1;
                     }
                 }
@@ -469,36 +479,38 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 const int key = s.kb0 + ch * kChunk + 16 * (lane & 7);
                 return id < 0 ? -1 : (id * c.Hkv + cur.g) * (c.page / 16) + (key & (c.page - 1)) / 16;
             };
-            // a thread's codes wait in shared memory of its own (16 bytes of each pass)
-            const uint32_t raw = L::raw + 16u * t;
+            // a thread's codes wait in shared memory of its own (16 bytes of each block)
+            const uint32_t raw = L::raw + 16u * lane, raw_v = raw + kChunk * D;
             auto load = [&](const uint8_t *src, uint32_t to, int ch, int block) {
                 if (ch < s.chunks) {
-                    const int left = s.ke - s.kb0 - ch * kChunk - key_in;      // keys from this thread's first one on
-                    const uint8_t *from = src + ((key_in % 16) * D + ck * 16);
+                    const int left = s.ke - s.kb0 - ch * kChunk;               // keys from the chunk's first one on
 #pragma unroll
-                    for (int i = 0; i < kPass; ++i) {
-                        const int b = __shfl_sync(0xffffffffu, block, (i * kRows + key_in) / 16);
-                        const bool in = b >= 0 && i * kRows < left;
-                        cp_async16_zfill(sb + to + i * (kConvThreads * 16), from + (int64_t)(in ? b : 0) * (16 * D), in);
+                    for (int i = 0; i < kTurns; ++i) {
+                        const int blk = i * kConvWarps + cw, kl = blk * kKeys + kr;
+                        const int b = __shfl_sync(0xffffffffu, block, kl / 16);
+                        const bool in = b >= 0 && kl < left;
+                        if (blk < kBlocks)
+                            cp_async16_zfill(sb + to + blk * 512, src + (int64_t)(in ? b : 0) * (16 * D) + (kl % 16) * D + ck * 16, in);
                     }
                 }
                 cp_async_commit();
             };
             auto put = [&](uint32_t off, uint32_t from) {
 #pragma unroll
-                for (int i = 0; i < kPass; ++i) {
-                    const int kl = i * kRows + key_in;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(base + from + i * (kConvThreads * 16));
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t o[8];
+                for (int i = 0; i < kTurns; ++i) {
+                    const int blk = i * kConvWarps + cw, kl = blk * kKeys + kr;
+                    if (blk < kBlocks) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(base + from + blk * 512);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t o[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) codes_to_f16<FMT>(w[e], o[2 * e], o[2 * e + 1]);
-                    *reinterpret_cast<uint4 *>(base + off + sw128<D>(kl, 2 * ck)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(base + off + sw128<D>(kl, 2 * ck + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                        for (int e = 0; e < 4; ++e) codes_to_f16<FMT>(w[e], o[2 * e], o[2 * e + 1]);
+                        *reinterpret_cast<uint4 *>(base + off + sw128<D>(kl, 2 * ck)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(base + off + sw128<D>(kl, 2 * ck + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
                 }
                 fence_async_smem();
             };
-            const uint32_t raw_v = raw + kChunk * D;
             int ids = ids_of(0), next = ids_of(1);
             int block = block_of(0, ids);
             load(c.k, raw, 0, block);
@@ -510,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 if (gi >= 2) ok = mbar_wait(bar(B_KEMPTY + st), ((gi >> 1) - 1) & 1, abort);
                 if (!ok) break;
                 // (S of chunk gi - 2 is complete, so the softmax is done with the scales of chunk gi - 4)
-                if (t < 32) {   // the chunk's scales
+                if (cw == 0) {   // the chunk's scales
                     float ks = 0.f, vs = 0.f;
                     if (ids >= 0) {
                         const int64_t at_s = (int64_t)ids * c.Hkv + cur.g;
@@ -550,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
     } else {
         // ------------------------------------------------------------ products
         tc::regs_down<64>();
-        if (warp == 12) {
+        {
             constexpr uint32_t idS = tc::idesc_f16(128, 128, false), idO = tc::idesc_f16(128, D, true);
             int gc = 0, cnt0 = 0, cnt1 = 0, nq0 = 0, nq1 = 0;
             // operands' descriptors: their low words are these, the high word is the same for all
@@ -639,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
     tc::fence_before();
     __syncthreads();
     if (tid == 0 && *abort) set_status(c.status, XGR_DEV_TIMEOUT);
-    if (warp == 12) {
+    if (warp == kIssueWarp) {
         tc::fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }

@@ -306,17 +306,39 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
 #pragma unroll
                 for (int r2 = 0; r2 < 2 * MT; ++r2) {
                     const int mt = r2 / 2, e0 = 2 * (r2 & 1);
+                    float most = 0.f;
 #pragma unroll
                     for (int nt = 0; nt < 4; ++nt) {
                         const float y = fac[r2] * ksc[nt / 2] * to2;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int key = key0 + nt * 8 + perm<D>(2 * qc + e);
-                            float x = s[mt][nt][e0 + e] * y;
-                            if (a.softcap > 0.f) x = up * tanh_score(x);
-                            if (a.slopes) x -= slope[r2] * fabsf((float)(pos[r2] - key));
-                            s[mt][nt][e0 + e] = x;
+                            s[mt][nt][e0 + e] *= y;
+                            most = fmaxf(most, fabsf(s[mt][nt][e0 + e]));
                         }
+                    }
+                    if (a.softcap > 0.f) {
+                        if (__all_sync(0xffffffffu, most <= kTanhNear)) {
+#pragma unroll
+                            for (int nt = 0; nt < 4; ++nt) {
+                                const float2 y = tc::fmul2(tanh_near(make_float2(s[mt][nt][e0], s[mt][nt][e0 + 1])), make_float2(up, up));
+                                s[mt][nt][e0] = y.x;
+                                s[mt][nt][e0 + 1] = y.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) s[mt][nt][e0 + e] = up * tanh_score(s[mt][nt][e0 + e]);
+                        }
+                    }
+                    if (a.slopes) {
+#pragma unroll
+                        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = key0 + nt * 8 + perm<D>(2 * qc + e);
+                                s[mt][nt][e0 + e] -= slope[r2] * fabsf((float)(pos[r2] - key));
+                            }
                     }
                     if (masked) {
 #pragma unroll

@@ -276,13 +276,34 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                         if (bad >> (2 * p + 1) & 1) seen &= 0x0000ffffu;
                         const float away_p = away - 32.f * p;
                         tc::wait_ld_into(x);
+                        float most = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float y = x[e] * (e < 16 ? k0 : k1);
-                            if (capped) y = up * tanh_score(y);
-                            if (a.slopes) y -= slope * fabsf(away_p - (float)e);
-                            x[e] = seen >> e & 1 ? y + (e < 16 ? g0.y : g1.y) : -INFINITY;
+                        for (int e = 0; e < 32; e += 2) {
+                            const float k = e < 16 ? k0 : k1;
+                            const float2 y = tc::fmul2(make_float2(x[e], x[e + 1]), make_float2(k, k));
+                            x[e] = y.x;
+                            x[e + 1] = y.y;
+                            most = fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y)));
                         }
+                        if (capped) {
+                            if (__all_sync(0xffffffffu, most <= kTanhNear)) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 y = tc::fmul2(tanh_near(make_float2(x[e], x[e + 1])), make_float2(up, up));
+                                    x[e] = y.x;
+                                    x[e + 1] = y.y;
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = up * tanh_score(x[e]);
+                            }
+                        }
+                        if (a.slopes) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] -= slope * fabsf(away_p - (float)e);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = seen >> e & 1 ? x[e] + (e < 16 ? g0.y : g1.y) : -INFINITY;
                         __syncwarp();
                         tc::st32(ts + 32u * p, reinterpret_cast<const uint32_t *>(x));
                     }

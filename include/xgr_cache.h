@@ -77,7 +77,7 @@ typedef struct {
 } xgr_cache;
 
 typedef struct {
-    int32_t n_rows;
+    int32_t n_rows;         /* up to 4194304 */
     int32_t max_pages;
     const int32_t *d_table; /* [n_rows][max_pages] */
     const int32_t *d_len;   /* [n_rows] */
@@ -144,8 +144,8 @@ xgr_status xgr_cache_store(const xgr_cache *cache, const xgr_cache_rows *rows, c
                            int64_t token_stride, int32_t *d_status, xgr_stream_t stream);
 
 /* The rows of the next step, from their parents: out row r continues row
- * d_parent[r] of `rows` (-1: an empty row) with room for d_n_new[r] more
- * tokens (NULL: none).  With p the parent's length:
+ * d_parent[r] of `rows` with room for d_n_new[r] more tokens (NULL: none);
+ * parent -1 makes an empty row without pages.  With p the parent's length:
  *   d_len_out[r] = p + d_n_new[r]
  *   full pages (p / page_size of them) are shared with the parent;
  *   a partly filled last page stays with the lowest out row that has it, unless

@@ -10,6 +10,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int kMaxPages = 1 << 30;
+constexpr int kMaxRows = 1 << 22;
 
 size_t up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 
@@ -38,7 +39,7 @@ xgr_status check_call(const xgr_cache *c, const xgr_cache_rows *rows, int32_t *d
     if (!al(c->d_k, 16) || !al(c->d_v, 16) || !al(c->d_k_scale, 4) || !al(c->d_v_scale, 4) || !al(d_status, 4))
         return XGR_ERR_ARG;
     if (!rows) return XGR_ERR_ARG;
-    if (rows->n_rows < 0 || rows->max_pages < 1) return XGR_ERR_SHAPE;
+    if (rows->n_rows < 0 || rows->n_rows > kMaxRows || rows->max_pages < 1) return XGR_ERR_SHAPE;
     if ((int64_t)rows->max_pages * c->page_size > 0x7fffffffll - 4096) return XGR_ERR_SHAPE;
     if (rows->n_rows > 0 && (!al(rows->d_table, 4) || !al(rows->d_len, 4))) return XGR_ERR_ARG;
     *a = CacheArgs{};
@@ -198,7 +199,7 @@ extern "C" xgr_status xgr_cache_fork(const xgr_cache *cache, const xgr_cache_row
     ForkArgs a{};
     const xgr_status st = check_call(cache, rows, d_status, &a.c);
     if (st != XGR_OK) return st;
-    if (n_out < 0) return XGR_ERR_SHAPE;
+    if (n_out < 0 || n_out > kMaxRows) return XGR_ERR_SHAPE;
     if (n_out == 0) return XGR_OK;
     if ((int64_t)n_out * 64 > 0x7fffffffll || (int64_t)n_out * rows->max_pages > 0x7fffffffll) return XGR_ERR_SHAPE;
     if (!al(d_parent, 4) || (d_n_new && !al(d_n_new, 4)) || !al(d_table_out, 4) || !al(d_len_out, 4) ||

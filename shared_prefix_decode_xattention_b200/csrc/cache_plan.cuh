@@ -222,7 +222,7 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_u
             if (u > 0 && units - u < a.lead) u = units;
         }
         sm.edge[e] = edge - left % units + u;
-        sm.first = Cursor{r, (int)t, min((int)(left / units), a.c.Hkv - 1), u, units};
+        if (e == 0) sm.first = Cursor{r, (int)t, min((int)(left / units), a.c.Hkv - 1), u, units};
     }
     __syncthreads();
     begin = sm.edge[0];

@@ -68,7 +68,7 @@ def test_struct_sizes(L):
     (dict(page_size=48), xgr.XGR_ERR_UNIMPLEMENTED), (dict(page_size=256), xgr.XGR_ERR_UNIMPLEMENTED),
     (dict(head_dim=96), xgr.XGR_ERR_UNIMPLEMENTED), (dict(format=2), xgr.XGR_ERR_ARG),
     (dict(n_pages=0), xgr.XGR_ERR_SHAPE), (dict(n_pages=(1 << 30) + 1), xgr.XGR_ERR_SHAPE),
-    (dict(n_kv_heads=0), xgr.XGR_ERR_SHAPE), (dict(d_k=None), xgr.XGR_ERR_ARG), (dict(d_v=D + 8), xgr.XGR_ERR_ARG),
+    (dict(n_kv_heads=0), xgr.XGR_ERR_SHAPE), (dict(n_pages=1 << 30, page_size=128), xgr.XGR_ERR_SHAPE), (dict(d_k=None), xgr.XGR_ERR_ARG), (dict(d_v=D + 8), xgr.XGR_ERR_ARG),
     (dict(d_v_scale=D + 2), xgr.XGR_ERR_ARG)])
 def test_bad_caches(L, call, bad, st):
     assert call(c=cache(**bad)) == st
@@ -76,7 +76,8 @@ def test_bad_caches(L, call, bad, st):
 
 @pytest.mark.parametrize("call", [attend, store, fork, compact])
 @pytest.mark.parametrize("bad,st", [
-    (dict(n_rows=-1), xgr.XGR_ERR_SHAPE), (dict(max_pages=0), xgr.XGR_ERR_SHAPE),
+    (dict(n_rows=-1), xgr.XGR_ERR_SHAPE), (dict(n_rows=(1 << 22) + 1), xgr.XGR_ERR_SHAPE),
+    (dict(max_pages=0), xgr.XGR_ERR_SHAPE),
     (dict(max_pages=1 << 25), xgr.XGR_ERR_SHAPE), (dict(d_table=None), xgr.XGR_ERR_ARG),
     (dict(d_len=D + 1), xgr.XGR_ERR_ARG)])
 def test_bad_rows(L, call, bad, st):

@@ -190,6 +190,93 @@ def test_attend_masked_nan_pages(n):
         close(out[::2], lse[::2], ref[::2], ref_lse[::2], vmax[::2], 128, 40.0)
 
 
+@pytest.mark.parametrize("most,G", [(1, 4), (9, 3), (40, 2)])
+def test_attend_many_ragged_rows(most, G):
+    """More rows (and tiles) than the plan has threads, rows without tokens and without keys among them."""
+    rng = np.random.default_rng(most)
+    n_rows = 2100 if most == 1 else 800
+    n = np.minimum(rng.integers(0, most + 1, n_rows), rng.integers(0, most + 1, n_rows))
+    lens = np.maximum(n, rng.integers(0, 60, n_rows))
+    lens[5], n[5] = 2500, most
+    attend_case(most, lens, n, 2, G, 16, 64, "int8" if most == 9 else "e4m3", extra=1, window=0 if most == 1 else 50)
+
+
+def test_attend_few_long_segments_of_many_rows():
+    """Few 256-row segments over long keys (equal parts), beside one with many (a line of units)."""
+    attend_case(1, [5000], [65], 1, 4, 128, 64, "int8", mask="full")                    # a whole tile and a narrow one
+    attend_case(2, [3000, 2000], [64, 128], 2, 2, 64, 128, "e4m3", mask="full")         # narrow, whole
+    attend_case(3, [400, 300, 260, 220, 1400], [260, 256, 200, 130, 300], 2, 2, 64, 64, "e4m3")
+
+
+def test_attend_captured_graphs_on_two_streams():
+    """Two graphs, captured on two streams of one cache, replayed at the same time."""
+    rng = np.random.default_rng(4)
+    cache = random_cache(rng, 300, 2, 32, 64, "e4m3")
+    pc = to_device(cache)
+    lens = np.array([4000, 3900])
+    t, ln = i32(random_table(rng, lens, 32, 300)), i32(lens)
+    runs = []
+    for n in (1, 50):
+        s, cu = torch.cuda.Stream(), i32([0, n, 2 * n])
+        q, _ = bf16(rng.standard_normal((2 * n, 4, 64)))
+        o, z = torch.empty_like(q), torch.empty((2 * n, 4), device="cuda")
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            pc.attend(t, ln, cu, q, o, z, max_q=n)
+        torch.cuda.synchronize()
+        want = o.clone(), z.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(20):
+                pc.attend(t, ln, cu, q, o, z, max_q=n)
+        runs.append((s, g, o, z, want, cu, q))
+    for _ in range(5):
+        for s, g, o, z, *_ in runs:
+            with torch.cuda.stream(s):
+                o.zero_()
+                g.replay()
+        torch.cuda.synchronize()
+        for s, g, o, z, want, *_ in runs:
+            assert torch.equal(o, want[0]) and torch.equal(z, want[1])
+    assert pc.device_status() == 0
+
+
+def test_calls_from_two_threads():
+    """Host threads with a stream each use one cache at the same time."""
+    import threading
+    rng = np.random.default_rng(4)
+    cache = random_cache(rng, 300, 2, 32, 64, "int8")
+    pc = to_device(cache)
+    lens = np.array([3000, 2900])
+    t, ln = i32(random_table(rng, lens, 32, 300)), i32(lens)
+    q, _ = bf16(rng.standard_normal((80, 4, 64)))
+    ref = {}
+    for n in (1, 40):
+        o, z = torch.empty_like(q[:2 * n]), torch.empty((2 * n, 4), device="cuda")
+        pc.attend(t, ln, i32([0, n, 2 * n]), q[:2 * n], o, z, max_q=n)
+        ref[n] = o
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(n):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            cu = i32([0, n, 2 * n])
+            o, z = torch.empty_like(q[:2 * n]), torch.empty((2 * n, 4), device="cuda")
+            for _ in range(50):
+                o.zero_()
+                pc.attend(t, ln, cu, q[:2 * n], o, z, max_q=n)
+                s.synchronize()
+                if not torch.equal(o, ref[n]):
+                    bad.append(n)
+    threads = [threading.Thread(target=work, args=(n,)) for n in (1, 40, 1, 40)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not bad and pc.device_status() == 0
+
+
 def test_attend_strided_queries_and_spare_tokens():
     """q as a slice of a fused projection; tokens behind the last row stay as they are."""
     rng = np.random.default_rng(1)

@@ -473,40 +473,53 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
         const bool all = cur.u == 0 && u1 == cur.units;   // the whole segment was this block's
         const int slot = cur.u == 0 ? 1 : 0;
         const float *obase = reinterpret_cast<const float *>(smem_raw);
+        // a thread a row: the warps' factors (over their m), and the row's sum
+        const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * R;
+        auto out_row = [&](int ia) { return (int64_t)(row.t0 + ia / a.G) * a.Hq + cur.g * a.G + ia % a.G; };
+        if (tid < R) {
+            float mm = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, sm.m[k][tid]);
+            const float ref = mm == -INFINITY ? 0.f : mm;
+            float f[kWarps], lsum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                f[k] = exp2_fast(sm.m[k][tid] - ref);
+                lsum += sm.l[k][tid] * f[k];
+            }
+            const float scale = !all ? 1.f : lsum == 0.f ? 0.f : 1.f / lsum;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) sm.m[k][tid] = f[k] * sm.vref[k] * scale;
+            const int ia = cur.t * R + tid;
+            if (ia < row.n * a.G) {
+                if (all) a.lse[out_row(ia)] = lsum == 0.f ? -INFINITY : (ref - kBias + log2f(lsum)) * kLn2;
+                else po.ml[part + tid] = make_float2(mm, lsum);
+            }
+        }
+        __syncthreads();
         for (int idx = tid; idx < R * D / 8; idx += kThreads) {
             const int rr = idx / (D / 8), d = (idx % (D / 8)) * 8;
             const int ia = cur.t * R + rr;
-            if (ia >= row.n * a.G) continue;
-            float mm = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, sm.m[k][rr]);
-            const float ref = mm == -INFINITY ? 0.f : mm;
-            float lsum = 0.f, x[8] = {};
+            if (ia >= row.n * a.G) break;                          // (rows ascend)
+            float x[8] = {};
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
-                const float f = exp2_fast(sm.m[k][rr] - ref);
-                lsum += sm.l[k][rr] * f;
-                const float fv = f * sm.vref[k];
+                const float fv = sm.m[k][rr];
                 const float4 y0 = *reinterpret_cast<const float4 *>(obase + (k * R + rr) * D + d);
                 const float4 y1 = *reinterpret_cast<const float4 *>(obase + (k * R + rr) * D + d + 4);
                 x[0] += y0.x * fv; x[1] += y0.y * fv; x[2] += y0.z * fv; x[3] += y0.w * fv;
                 x[4] += y1.x * fv; x[5] += y1.y * fv; x[6] += y1.z * fv; x[7] += y1.w * fv;
             }
             if (all) {
-                const int64_t oi = (int64_t)(row.t0 + ia / a.G) * a.Hq + cur.g * a.G + ia % a.G;
-                const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
                 uint4 pk;
                 __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&pk);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(x[2 * e] * inv, x[2 * e + 1] * inv);
-                *reinterpret_cast<uint4 *>(a.out + oi * D + d) = pk;
-                if (d == 0) a.lse[oi] = lsum == 0.f ? -INFINITY : (ref - kBias + log2f(lsum)) * kLn2;
+                for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+                *reinterpret_cast<uint4 *>(a.out + out_row(ia) * D + d) = pk;
             } else {
-                const int64_t pi = ((int64_t)blockIdx.x * 2 + slot) * R + rr;
-                float4 *dst = reinterpret_cast<float4 *>(po.o + pi * D + d);
+                float4 *dst = reinterpret_cast<float4 *>(po.o + (part + rr) * D + d);
                 dst[0] = make_float4(x[0], x[1], x[2], x[3]);
                 dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-                if (d == 0) po.ml[pi] = make_float2(mm, lsum);
             }
         }
         __syncthreads();   // the rings and (m, l) are free for the next segment

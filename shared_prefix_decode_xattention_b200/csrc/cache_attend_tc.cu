@@ -405,10 +405,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 const int64_t pi = ((int64_t)blockIdx.x * 2 + (cur.u == 0 ? 1 : 0)) * R + tr + 128 * h;
                 const float ref = M == -INFINITY ? 0.f : M;
                 const float scale = !all ? 1.f : l == 0.f ? 0.f : 1.f / l;
-                // rows go out through the warp's share of the Q tile (no product reads it any more), 2 D bytes a
-                // row at a time, so that stores are whole lines
-                uint8_t *stage = base + L::q + h * L::kTile + (warp & 3) * (L::kTile / 4);
-                auto slot = [&](int row, int ch) { return stage + row * (2 * D) + ((ch ^ (row & 7)) << 4); };
+                // rows go out through the warp's own rows of the Q tile (no product reads them any more; another warp
+                // may be filling its own for the next segment already), 2 D bytes a row at a time, so that stores are
+                // whole lines
+                auto slot = [&](int row, int ch) {
+                    return base + L::q + h * L::kTile + sw128<D>(32 * (warp & 3) + row, ch);
+                };
                 auto flush = [&](uint8_t *dst, int64_t row_bytes, int64_t my_row) {   // lane's row of the result (-1: none)
                     __syncwarp();
 #pragma unroll 4

@@ -319,6 +319,34 @@ def test_attend_is_the_same_twice_and_on_other_streams():
     assert pc.device_status() == 0
 
 
+@pytest.mark.parametrize("d,G,lo,hi", [(128, 2, 4, 14), (128, 2, 20, 40), (64, 2, 4, 16), (128, 4, 1, 4), (64, 4, 30, 200),
+                                       (128, 4, 40, 300)])
+def test_attend_is_the_same_every_time(d, G, lo, hi):
+    """Ragged rows, many segments a CTA, cut ones among them, some hundred times: a race would show."""
+    rng = np.random.default_rng(hi)
+    n_rows, hkv, page = 99, 8, 128
+    n = rng.integers(lo, hi + 1, n_rows)
+    lens = np.maximum(n, rng.integers(18, 1815, n_rows))
+    n_pages = int(sum(-(-int(x) // page) for x in lens)) + 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    from shared_prefix_decode_xattention_b200.cache import PagedCache
+    k, v = (torch.randint(-127, 128, (n_pages, hkv, page, d), generator=g, device="cuda", dtype=torch.int8) for _ in range(2))
+    ks, vs = (torch.rand((n_pages, hkv), generator=g, device="cuda") / 73 for _ in range(2))
+    pc = PagedCache(k, v, ks, vs)
+    t, ln, cu = i32(random_table(rng, lens, page, n_pages)), i32(lens), i32(np.concatenate([[0], np.cumsum(n)]))
+    T = int(n.sum())
+    q = torch.randn((T, hkv * G, d), generator=g, device="cuda").to(torch.bfloat16)
+    o, z = torch.empty_like(q), torch.empty((T, hkv * G), device="cuda")
+    pc.attend(t, ln, cu, q, o, z, max_q=hi)
+    first = o.clone(), z.clone()
+    same = torch.ones((), dtype=torch.bool, device="cuda")
+    for _ in range(300):
+        o.zero_()
+        pc.attend(t, ln, cu, q, o, z, max_q=hi)
+        same &= (o == first[0]).all() & (z == first[1]).all()
+    assert same.item() and pc.device_status() == 0
+
+
 def test_attend_captured_and_replayed():
     """A graph follows the lengths, tables and queries in its buffers; a capture without a workspace is refused."""
     rng = np.random.default_rng(1)

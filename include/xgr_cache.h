@@ -45,6 +45,7 @@
  * never cleared by these calls), and the faulty element is skipped: a key in a
  * page that is not there is not attended, a token without a page is not
  * stored, a row whose d_cu or length is at fault has no tokens.
+ * XGR_DEV_TIMEOUT, as in xgr.h: a bounded wait inside xgr_cache_attend gave up.
  * The workspace of a call (d_ws, 256-byte aligned, at least the bytes its
  * _bytes function gives) needs no initial contents and holds nothing between
  * calls, so calls on one stream may share it; calls that may overlap on the

@@ -33,9 +33,12 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return lo | hi << 16;
 }
 
+// |x| <= 127, by the choice of the scale: adding 1.5 * 2^23 rounds to the nearest
+// whole number, ties to even, and leaves it in the low byte (the conversion
+// instruction runs at an eighth of the rate: 355 against 306 us for 590k tokens)
 __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
-    auto q = [](float x) { return (uint32_t)(uint8_t)(int8_t)max(-127, min(127, __float2int_rn(x))); };
-    return q(a) | q(b) << 8 | q(c) << 16 | q(d) << 24;
+    auto q = [](float x) { return __float_as_uint(x + 12582912.f); };
+    return __byte_perm(__byte_perm(q(a), q(b), 0x0040), __byte_perm(q(c), q(d), 0x0040), 0x5410);
 }
 
 template <int FMT>
@@ -126,11 +129,12 @@ __global__ void __launch_bounds__(kThreads) cache_store_kernel(StoreArgs a, int 
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {   // magnitudes of bf16 pairs compare as whole numbers, NaN and infinity above all
             const uint32_t w[4] = {x[i][h].x, x[i][h].y, x[i][h].z, x[i][h].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+            for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
         }
+    top = max(top & 0xffffu, top >> 16);
     top = __reduce_max_sync(0xffffffffu, top);
     if constexpr (W > 1) {
         if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
@@ -143,8 +147,8 @@ __global__ void __launch_bounds__(kThreads) cache_store_kernel(StoreArgs a, int 
     const bool sick = poison || was != was;   // a NaN scale stays until the page is begun anew
     const float scale = sick ? __int_as_float(0x7fc00000) : fmaxf(want, was);
     const bool grown = t_lo > 0 && scale != was && !(was != was);
-    // a power of two divides exactly by multiplying with its inverse
-    const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
+    // a power of two (all this kernel writes) divides exactly by multiplying with its inverse
+    const bool pow2 = sick || (__float_as_uint(scale) & 0x7fffffu) == 0;
     const float inv = 1.f / scale;
     auto quot = [&](float v) { return sick ? 0.f : pow2 ? v * inv : __fdiv_rn(v, scale); };
     if (tid == 0) *scale_at = scale;
@@ -156,12 +160,27 @@ __global__ void __launch_bounds__(kThreads) cache_store_kernel(StoreArgs a, int 
         uint4 *d = reinterpret_cast<uint4 *>(dst + ch * 16);
         if (t >= t_lo && t < t_hi) {
             uint32_t o[4];
+            if (pow2) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float f[8];
-                unpack8(x[i][h], f);
-                o[2 * h] = pack4<FMT>(quot(f[0]), quot(f[1]), quot(f[2]), quot(f[3]));
-                o[2 * h + 1] = pack4<FMT>(quot(f[4]), quot(f[5]), quot(f[6]), quot(f[7]));
+                for (int h = 0; h < 2; ++h) {
+                    float f[8];
+                    unpack8(x[i][h], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] *= inv;
+                    o[2 * h] = pack4<FMT>(f[0], f[1], f[2], f[3]);
+                    o[2 * h + 1] = pack4<FMT>(f[4], f[5], f[6], f[7]);
+                }
+                if (sick) o[0] = o[1] = o[2] = o[3] = 0;
+            } else {   // a larger scale of older tokens, from another quantiser
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float f[8];
+                    unpack8(x[i][h], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = __fdiv_rn(f[e], scale);
+                    o[2 * h] = pack4<FMT>(f[0], f[1], f[2], f[3]);
+                    o[2 * h + 1] = pack4<FMT>(f[4], f[5], f[6], f[7]);
+                }
             }
             *d = make_uint4(o[0], o[1], o[2], o[3]);
         } else if (t < t_lo && grown) {

@@ -105,7 +105,8 @@ typedef struct {
  *   d_q    bf16, query head h of token t at d_q + t * q_stride + h * head_dim
  *          (q_stride in elements, a multiple of 8, >= n_q_heads * head_dim);
  *          head h reads kv head h / (n_q_heads / n_kv_heads)
- *   d_out  bf16 [n_tokens][n_q_heads][head_dim]; d_lse fp32 [n_tokens][n_q_heads]
+ *   d_out  bf16 [n_tokens][n_q_heads][head_dim]; d_lse fp32 [n_tokens][n_q_heads]; neither
+ *          overlaps an input
  * Query i of a row sees the keys lo <= j < hi: hi = len (full), pos + 1
  * (causal), max(pos + 1, min(prefix, len)) (causal with a prefix); lo = the
  * largest of 0, d_first and pos - window + 1.  A query that sees none gets 0

@@ -103,6 +103,9 @@ extern "C" xgr_status xgr_cache_attend(const xgr_cache *cache, const xgr_cache_r
     if (q_stride < (int64_t)n_q_heads * cache->head_dim || q_stride % 8) return XGR_ERR_SHAPE;
     if ((int64_t)n_tokens * n_q_heads > 0x7fffffffll || (int64_t)max_q * G > 0x3fffffffll) return XGR_ERR_SHAPE;
     if (!al(d_cu, 4) || !al(d_q, 16) || !al(d_out, 16) || !al(d_lse, 4) || !al(d_ws, kAlign)) return XGR_ERR_ARG;
+    // (the query of a token is read by whoever takes a part of its keys)
+    const size_t q_bytes = ((size_t)(n_tokens - 1) * q_stride + (size_t)n_q_heads * cache->head_dim) * 2;
+    if (overlaps(d_out, (size_t)n_tokens * n_q_heads * cache->head_dim * 2, d_q, q_bytes)) return XGR_ERR_ARG;
     if (ws_bytes < attend_ws_bytes(cache->head_dim, G, rows->n_rows, n_tokens)) return XGR_ERR_CAPACITY;
     a.c.cu = d_cu;
     a.c.n_tokens = n_tokens;

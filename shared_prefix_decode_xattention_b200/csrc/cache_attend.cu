@@ -24,6 +24,11 @@
 // dims of four keys: conversion needs no shuffles, the weights' fragments are
 // the scores' own registers, and all shared-memory reads are 16 bytes wide and
 // free of bank conflicts (perm and swz below).
+//
+// Measured: 64 rows of one token over 8.4k-10.2k e4m3 keys (1.23 GB, 32 / 8 heads,
+// D = 128): 214 us, 5.7 TB/s; capped 238 us.  Three rows of 9k-180k int8 keys with a
+// distance bias (0.33 GB): 86 us.  Some 780 instructions a warp and tile keep half
+// of the issue slots busy, so what is left is latency and issue, not bytes alone.
 #include "cache_codes.cuh"
 #include "cache_plan.cuh"
 

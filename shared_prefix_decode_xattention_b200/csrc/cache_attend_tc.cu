@@ -31,8 +31,9 @@
 // scores may only be written once W V has read the weights over the old ones
 // (tensor memory is full: two S, two O of 128 columns); two tiles overlap their
 // chains.  Measured at 512 beams x 32 heads over 4096 keys, 16 requests (550
-// GFLOP; 1692 TFLOP/s of bf16 would take 325 us): 684 us, 805 TFLOP/s, 0.48 of the
-// measured bf16 rate; four conversion warps 696 us, three 870; weights through
+// GFLOP; 1692 TFLOP/s of bf16 would take 325 us): 692 us, 795 TFLOP/s, 0.47 of the
+// measured bf16 rate (742 us where hundreds run back to back and the clock settles
+// lower); four conversion warps 696 us, three 870; weights through
 // shared memory instead, so that the next scores need not wait, 740 us (the
 // writes, and single operand buffers for want of room); the scores read in two
 // rolled passes 790 us; spills in the issuing warp (48 registers) 822 us.
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 const bool slow = masked || capped || a.slopes;
                 // Scores to exponents of weights, in place.  (Rolled: this and the body below, both unrolled, are longer
                 // than the instruction caches next to the schedulers, and waiting for instructions cost more than the
-                // second reading: 374 against 342 us for capped, masked chunks of 3700 tokens.)
+                // second reading: 372 against 339 us for capped, masked chunks of 3700 tokens.)
                 if (slow) {
                     const float up = a.softcap * kLog2e;
                     const float away = (float)(pos - key0);

@@ -28,7 +28,7 @@ def rows(**kw):
 
 
 def attend(c=None, r=None, o=None, **kw):
-    a = dict(cu=D, n_tokens=3, max_q=1, hq=16, q=D, stride=16 * 128, out=D, lse=D, ws=D, ws_bytes=1 << 40, status=D)
+    a = dict(cu=D, n_tokens=3, max_q=1, hq=16, q=D, stride=16 * 128, out=2 * D, lse=D, ws=D, ws_bytes=1 << 40, status=D)
     a.update(kw)
     opts = xgr.xgr_attn_opts(**{**dict(scale=0, softcap=0, mask=1, window=0), **(o or {})})
     return xgr.lib().xgr_cache_attend(ctypes.byref(c or cache()), ctypes.byref(r or rows()), a["cu"], a["n_tokens"],
@@ -92,7 +92,7 @@ def test_status_word_is_needed(L, call):
 @pytest.mark.parametrize("kw,o,st", [
     (dict(hq=18), {}, xgr.XGR_ERR_SHAPE), (dict(hq=0), {}, xgr.XGR_ERR_SHAPE), (dict(stride=2040), {}, xgr.XGR_ERR_SHAPE),
     (dict(stride=2052), {}, xgr.XGR_ERR_SHAPE), (dict(n_tokens=-1), {}, xgr.XGR_ERR_SHAPE), (dict(max_q=-1), {}, xgr.XGR_ERR_SHAPE),
-    (dict(q=D + 8), {}, xgr.XGR_ERR_ARG), (dict(out=None), {}, xgr.XGR_ERR_ARG), (dict(lse=D + 2), {}, xgr.XGR_ERR_ARG),
+    (dict(q=D + 8), {}, xgr.XGR_ERR_ARG), (dict(out=D + 4096), {}, xgr.XGR_ERR_ARG), (dict(out=None), {}, xgr.XGR_ERR_ARG), (dict(lse=D + 2), {}, xgr.XGR_ERR_ARG),
     (dict(cu=None), {}, xgr.XGR_ERR_ARG), (dict(ws=D + 16), {}, xgr.XGR_ERR_ARG), (dict(ws_bytes=1000), {}, xgr.XGR_ERR_CAPACITY),
     ({}, dict(mask=2), xgr.XGR_ERR_ARG), ({}, dict(mask=0, d_prefix=D), xgr.XGR_ERR_ARG), ({}, dict(window=-1), xgr.XGR_ERR_SHAPE),
     ({}, dict(softcap=-1.0), xgr.XGR_ERR_ARG), ({}, dict(softcap=float("nan")), xgr.XGR_ERR_ARG),

@@ -6,13 +6,14 @@ The order of a decode step: ``fork`` (the rows' new parents, pages for the
 tokens to come), ``store``, ``attend``, a selection.
 
 Streams: a call runs on ``stream``, or on torch's current stream of the cache's
-device.  Each stream has workspaces of its own, so calls on two streams may
-overlap; a captured graph keeps using the workspaces of the stream it was
-captured on, so two graphs that may run at the same time are captured on two
-streams, or with a PagedCache each (over the same tensors).  A workspace is made
-by the first call that needs it and never freed before the PagedCache; a call
-under capture that would have to make one raises, so make the call once before
-the capture, on the capturing stream.
+device.  Each stream has a workspace of its own, so calls on two streams may
+overlap.  It is made by the first call that needs it and never freed before the
+PagedCache.  A captured graph keeps using the workspace of the stream it was
+captured on; a call under capture that would have to make one raises.  So either
+make the call once before the capture, on the capturing stream, or give the
+captured calls a ``workspace`` of their own (a uint8 tensor of attend_bytes /
+fork_bytes / compact_bytes; calls of one graph may share it), which is also the
+way for graphs that may run at the same time.
 """
 from __future__ import annotations
 
@@ -108,13 +109,17 @@ class PagedCache:
             need = self._need[key] = size()
         return need
 
-    def _workspace(self, fn, stream, need):
+    def _workspace(self, fn, stream, need, given):
+        if given is not None:
+            if given.dtype is not self._torch.uint8 or given.get_device() != self._index or not given.is_contiguous():
+                _bad(fn, f"workspace: contiguous uint8 on {self.device}")
+            return given, given.numel(), given.data_ptr()     # (the library checks size and alignment)
         ws = self._ws.get(stream)
         if ws is None or ws[1] < need:
             torch = self._torch
             if torch.cuda.is_current_stream_capturing():
-                _bad(fn, "no workspace of this size on the capturing stream yet: make the call once "
-                         "before the capture", xgr.XGR_ERR_STATE)
+                _bad(fn, "no workspace of this size on the capturing stream yet: make the call once on it "
+                         "before the capture, or pass workspace", xgr.XGR_ERR_STATE)
             if ws is not None:
                 self._old.append(ws[0])
                 need = max(need, 2 * ws[1])
@@ -131,17 +136,31 @@ class PagedCache:
             return call(*args)
 
     # ------------------------------------------------------------------ calls
+    def attend_bytes(self, n_q_heads: int, n_rows: int, n_tokens: int) -> int:
+        """Bytes of the workspace of an attend call."""
+        return self._bytes(("attend", n_q_heads, n_rows, n_tokens),
+                           lambda: xgr.xgr_cache_attend_bytes(self._c, n_q_heads, n_rows, n_tokens))
+
+    def fork_bytes(self, n_rows: int, n_out: int) -> int:
+        """Bytes of the workspace of a fork of n_rows rows into n_out."""
+        return self._bytes(("fork", n_rows, n_out), lambda: xgr.xgr_cache_fork_bytes(self._c, n_rows, n_out))
+
+    def compact_bytes(self) -> int:
+        """Bytes of the workspace of a compaction."""
+        return self._bytes("compact", lambda: xgr.xgr_cache_compact_bytes(self._c))
+
     def attend(self, table, length, cu, q, out, lse, *, max_q: int, scale: float = 0.0, softcap: float = 0.0,
-               mask: str = "causal", window: int = 0, slopes=None, prefix=None, first=None, stream=None):
+               mask: str = "causal", window: int = 0, slopes=None, prefix=None, first=None, stream=None,
+               workspace=None):
         """Attention of packed query tokens q [T][Hq][D] (bf16) over the rows' pages into out
         [T][Hq][D] (bf16) and lse [T][Hq] (fp32); cu int32 [n_rows + 1].  mask: "full", "causal",
         or "prefix" (causal beside a bidirectional prefix of prefix[r] tokens).  See
         xgr_cache_attend."""
         self._run(self._attend, table, length, cu, q, out, lse, max_q, scale, softcap, mask, window, slopes,
-                  prefix, first, stream)
+                  prefix, first, stream, workspace)
 
     def _attend(self, table, length, cu, q, out, lse, max_q, scale, softcap, mask, window, slopes, prefix,
-                first, stream):
+                first, stream, workspace):
         fn, index = "PagedCache.attend", self._index
         rows = self._rows(fn, table, length)
         n_rows = rows.n_rows
@@ -166,10 +185,8 @@ class PagedCache:
             opts.d_prefix = self._int32(fn, "prefix", prefix, (n_rows,))
         if first is not None:
             opts.d_first = self._int32(fn, "first", first, (n_tokens,))
-        need = self._bytes(("attend", hq, n_rows, n_tokens),
-                           lambda: xgr.xgr_cache_attend_bytes(self._c, hq, n_rows, n_tokens))
         st = self._stream(stream)
-        _, size, d_ws = self._workspace(fn, st, need)
+        _, size, d_ws = self._workspace(fn, st, self.attend_bytes(hq, n_rows, n_tokens), workspace)
         xgr.xgr_cache_attend(self._c, rows, d_cu, n_tokens, max_q, hq, q.data_ptr(), stride, opts,
                              out.data_ptr(), lse.data_ptr(), d_ws, size, self._d_status, st)
 
@@ -188,12 +205,12 @@ class PagedCache:
         xgr.xgr_cache_store(self._c, rows, d_cu, k.shape[0], max_n, k.data_ptr(), v.data_ptr(), stride,
                             self._d_status, self._stream(stream))
 
-    def fork(self, table, length, parent, n_new, table_out, len_out, *, stream=None):
+    def fork(self, table, length, parent, n_new, table_out, len_out, *, stream=None, workspace=None):
         """The rows of the next step from their parents (-1: none), with pages for n_new[r] more
         tokens (None: none).  See xgr_cache_fork."""
-        self._run(self._fork, table, length, parent, n_new, table_out, len_out, stream)
+        self._run(self._fork, table, length, parent, n_new, table_out, len_out, stream, workspace)
 
-    def _fork(self, table, length, parent, n_new, table_out, len_out, stream):
+    def _fork(self, table, length, parent, n_new, table_out, len_out, stream, workspace):
         fn = "PagedCache.fork"
         rows = self._rows(fn, table, length)
         if parent.dim() != 1:
@@ -203,25 +220,22 @@ class PagedCache:
         d_new = None if n_new is None else self._int32(fn, "n_new", n_new, (n_out,))
         d_table = self._int32(fn, "table_out", table_out, (n_out, rows.max_pages))
         d_len = self._int32(fn, "len_out", len_out, (n_out,))
-        need = self._bytes(("fork", rows.n_rows, n_out),
-                           lambda: xgr.xgr_cache_fork_bytes(self._c, rows.n_rows, n_out))
         st = self._stream(stream)
-        _, size, d_ws = self._workspace(fn, st, need)
+        _, size, d_ws = self._workspace(fn, st, self.fork_bytes(rows.n_rows, n_out), workspace)
         xgr.xgr_cache_fork(self._c, rows, n_out, d_parent, d_new, d_table, d_len, d_ws, size, self._d_status, st)
 
-    def compact(self, table, length, table_out, n_used, *, stream=None):
+    def compact(self, table, length, table_out, n_used, *, stream=None, workspace=None):
         """Moves the pages that the rows hold to the front; n_used int32 [1].  See
         xgr_cache_compact."""
-        self._run(self._compact, table, length, table_out, n_used, stream)
+        self._run(self._compact, table, length, table_out, n_used, stream, workspace)
 
-    def _compact(self, table, length, table_out, n_used, stream):
+    def _compact(self, table, length, table_out, n_used, stream, workspace):
         fn = "PagedCache.compact"
         rows = self._rows(fn, table, length)
         d_table = self._int32(fn, "table_out", table_out, table.shape)
         d_used = self._int32(fn, "n_used", n_used, (1,))
-        need = self._bytes("compact", lambda: xgr.xgr_cache_compact_bytes(self._c))
         st = self._stream(stream)
-        _, size, d_ws = self._workspace(fn, st, need)
+        _, size, d_ws = self._workspace(fn, st, self.compact_bytes(), workspace)
         xgr.xgr_cache_compact(self._c, rows, d_table, d_used, d_ws, size, self._d_status, st)
 
     def device_status(self) -> int:

@@ -291,9 +291,9 @@ constexpr double tanh_coef(double c, int i) {   // c y^(2i + 1) as a factor of y
     return f;
 }
 __device__ __forceinline__ float2 tanh_near(float2 y2) {
-    constexpr float c0 = (float)tanh_coef(1.0, 0), c1 = (float)tanh_coef(-0.3333307206630707, 1),
-                    c2 = (float)tanh_coef(0.13324828445911407, 2), c3 = (float)tanh_coef(-0.05298924073576927, 3),
-                    c4 = (float)tanh_coef(0.017141319811344147, 4);
+    constexpr float c0 = (float)tanh_coef(1.0, 0), c1 = (float)tanh_coef(-0x1.5554a60000000p-2, 1),
+                    c2 = (float)tanh_coef(0x1.10e47a0000000p-3, 2), c3 = (float)tanh_coef(-0x1.b2167e0000000p-5, 3),
+                    c4 = (float)tanh_coef(0x1.18d7e80000000p-6, 4);
     const float2 u = tc::fmul2(y2, y2);
     float2 r = tc::ffma2(u, make_float2(c4, c4), make_float2(c3, c3));
     r = tc::ffma2(r, u, make_float2(c2, c2));

@@ -241,6 +241,63 @@ def test_attend_captured_graphs_on_two_streams():
     assert pc.device_status() == 0
 
 
+def test_whole_step_in_one_graph():
+    """Fork, store, attend and compact captured on torch's own capture stream with a workspace of their own, and
+    replayed on other inputs."""
+    rng = np.random.default_rng(4)
+    cache = random_cache(rng, 64, 2, 16, 64, "int8")
+    pc = to_device(cache)
+    rows, width = 6, 8
+    lens = np.array([40, 33, 64, 1, 80, 17], np.int32)
+    table = random_table(rng, lens, 16, 64, extra=3)
+    t, ln, par = i32(table), i32(lens), i32(np.arange(rows))
+    t2, l2, t3, used = i32(np.zeros((rows, width))), i32(np.zeros(rows)), i32(np.zeros((rows, width))), i32([0])
+    ones, cu = i32(np.ones(rows)), i32(np.arange(rows + 1))
+    k, _ = bf16(rng.standard_normal((rows, 2, 64)))
+    q, _ = bf16(rng.standard_normal((rows, 4, 64)))
+    o, z = torch.empty_like(q), torch.empty((rows, 4), device="cuda")
+    need = max(pc.attend_bytes(4, rows, rows), pc.fork_bytes(rows, rows), pc.compact_bytes())
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def step():
+        pc.fork(t, ln, par, ones, t2, l2, workspace=ws)
+        pc.store(t2, l2, cu, k, k, max_n=1)
+        pc.attend(t2, l2, cu, q, o, z, max_q=1, workspace=ws)
+        pc.compact(t2, l2, t3, used, workspace=ws)
+    with pytest.raises(xgr.XgrError) as e:
+        pc.fork(t, ln, par, ones, t2, l2, workspace=ws[:256])
+    assert e.value.status == xgr.XGR_ERR_CAPACITY
+    step()
+    torch.cuda.synchronize()
+    for x, c in (("k", pc.k), ("v", pc.v)):
+        c.view(torch.uint8).copy_(torch.from_numpy(cache[x]))
+    pc.k_scale.copy_(torch.from_numpy(cache["ks"]))
+    pc.v_scale.copy_(torch.from_numpy(cache["vs"]))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(2):
+        parent = rng.integers(0, rows, rows).astype(np.int32)
+        par.copy_(i32(parent))
+        k2, k64 = bf16(rng.standard_normal((rows, 2, 64)))
+        q2, q64 = bf16(rng.standard_normal((rows, 4, 64)))
+        k.copy_(k2)
+        q.copy_(q2)
+        t.copy_(i32(table))
+        ln.copy_(i32(lens))
+        g.replay()
+        torch.cuda.synchronize()
+        want_t, want_l, _ = oc.fork(cache, table, lens, parent, np.ones(rows, np.int32))
+        oc.store(cache, want_t, want_l, np.arange(rows + 1), k64, k64)
+        ref, ref_lse = oc.attend(cache, want_t, want_l, np.arange(rows + 1), q64)
+        close(o, z, ref, ref_lse, np.full((rows, 4, 1), 16.0), 64, 40.0)
+        table, u = oc.compact(cache, want_t, want_l)
+        lens = want_l
+        assert np.array_equal(t3.cpu().numpy(), table) and used.item() == u
+        same_cache(to_host(pc), cache)
+    assert pc.device_status() == 0
+
+
 def test_calls_from_two_threads():
     """Host threads with a stream each use one cache at the same time."""
     import threading

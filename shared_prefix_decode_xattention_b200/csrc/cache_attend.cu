@@ -636,9 +636,14 @@ __global__ void __launch_bounds__(128) cache_tile_lo_kernel(AttendArgs a, int R,
 constexpr int kSmallCtas = 3 * kSms;         // 16-row tiles: three CTAs an SM
 constexpr int kWideCtas = 2 * kSms;          // 32-row tiles: two
 constexpr int kTcRows256 = 256;              // tcgen05 tiles: one
-constexpr int kMinUnits = 4;                 // fewest units a CTA takes (512 keys): below, joining costs more than it spreads
-constexpr int kTcLead = 3;                   // a 256-row segment's rows and result cost about as much as three units
-constexpr int kWholeUnits = 8;               // rows of at most this many units are not cut
+// Fewest units a CTA takes: one row of 9300 keys takes 23.7 us with 4, 23.2 with 2, 27.2 with 8; four rows of 1000 to
+// 2000 keys 20.6, 20.9, 26.5.
+constexpr int kMinUnits = 4;
+// A 256-row segment's rows and result cost about as much as three units: packed chunks of 3700 tokens, uncapped, 192 us
+// with 3, 207 with 2, 231 with 1, 291 with none.
+constexpr int kTcLead = 3;
+// Rows of at most this many units are not cut and need no join: 200 rows of 300 to 800 keys 85 us, cut and joined 91.
+constexpr int kWholeUnits = 8;
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -687,7 +692,9 @@ cudaError_t launch_cache_attend(const AttendArgs &in, cudaStream_t s) {
     AttendArgs a = in;
     const CacheArgs &c = a.c;
     a.whole = (int64_t)c.max_pages * c.page <= kWholeUnits * kUnitKeys;
-    // 16 or 32 query rows a tile on mma.sync while no row has more; else 256 a tile on tcgen05
+    // 16 or 32 query rows a tile on mma.sync while no row has more; else 256 a tile on tcgen05.  Measured on 64 rows
+    // over 8.4k-10.2k keys: 16 query rows 215 us in 16-row tiles, 325 in 32-row ones; 32 query rows 344 us in 32-row
+    // tiles, 592 on tcgen05; 64 query rows 652 us in two 32-row tiles, 596 on tcgen05.
     const int64_t most = (int64_t)a.max_q * a.G;
     const int R = most <= 16 ? 16 : most <= 32 ? 32 : kTcRows256;
     const int cap = R == 16 ? kSmallCtas : R == 32 ? kWideCtas : kSms;

@@ -58,7 +58,7 @@ constexpr float kMinLogV = -100.f;             // log2 of the smallest V scale t
 struct Scales {
     float2 k[8];                // by 16 keys: K scale, log2 V scale
     float iv[8];                // 1 / V scale
-    int bad;                    // bit g: group g lies in a page that is not there; bit 8: a V scale is NaN
+    int bad;                    // bit g: group g lies in a page that is not there; bit 8: a scale is NaN (the slow way)
     int pad[3];
 };
 

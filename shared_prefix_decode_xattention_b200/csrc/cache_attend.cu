@@ -636,12 +636,14 @@ __global__ void __launch_bounds__(128) cache_tile_lo_kernel(AttendArgs a, int R,
 constexpr int kSmallCtas = 3 * kSms;         // 16-row tiles: three CTAs an SM
 constexpr int kWideCtas = 2 * kSms;          // 32-row tiles: two
 constexpr int kTcRows256 = 256;              // tcgen05 tiles: one
-// Fewest units a CTA takes: one row of 9300 keys takes 23.7 us with 4, 23.2 with 2, 27.2 with 8; four rows of 1000 to
-// 2000 keys 20.6, 20.9, 26.5.
+// Fewest units a CTA takes: one row of 9300 keys takes 24.4 us with 4, 23.9 with 2, 27.7 with 8; four rows of 1000 to
+// 2000 keys 21.0, 21.4, 27.1.
 constexpr int kMinUnits = 4;
-// A 256-row segment's rows and result cost about as much as three units: packed chunks of 3700 tokens, uncapped, 192 us
-// with 3, 207 with 2, 231 with 1, 291 with none.
+// A 256-row segment's rows and result cost about as much as three units of its keys, and as two where a cap makes keys
+// dearer.  7 and 12 packed chunks of 61 to 1000 tokens: without a cap 183 and 311 us with 3, 195 and 324 with 2 (7: 216
+// with 1); with a cap 212 and 358 with 2, 222 and 373 with 3 (7: 234 with 1).  Equal chunks differ by less than 2%.
 constexpr int kTcLead = 3;
+constexpr int kTcLeadCapped = 2;
 // Rows of at most this many units are not cut and need no join: 200 rows of 300 to 800 keys 85 us, cut and joined 91.
 constexpr int kWholeUnits = 8;
 
@@ -693,12 +695,12 @@ cudaError_t launch_cache_attend(const AttendArgs &in, cudaStream_t s) {
     const CacheArgs &c = a.c;
     a.whole = (int64_t)c.max_pages * c.page <= kWholeUnits * kUnitKeys;
     // 16 or 32 query rows a tile on mma.sync while no row has more; else 256 a tile on tcgen05.  Measured on 64 rows
-    // over 8.4k-10.2k keys: 16 query rows 215 us in 16-row tiles, 325 in 32-row ones; 32 query rows 344 us in 32-row
-    // tiles, 592 on tcgen05; 64 query rows 652 us in two 32-row tiles, 596 on tcgen05.
+    // over 8.4k-10.2k keys, no cap: 16 query rows 224 us in 16-row tiles, 333 in 32-row ones; 32 query rows 344 us in
+    // 32-row tiles, 592 on tcgen05; 64 query rows 652 us in two 32-row tiles, 596 on tcgen05.
     const int64_t most = (int64_t)a.max_q * a.G;
     const int R = most <= 16 ? 16 : most <= 32 ? 32 : kTcRows256;
     const int cap = R == 16 ? kSmallCtas : R == 32 ? kWideCtas : kSms;
-    a.lead = R == kTcRows256 && !a.whole ? kTcLead : 0;
+    a.lead = R != kTcRows256 || a.whole ? 0 : a.softcap > 0.f ? kTcLeadCapped : kTcLead;
     const int min_units = a.whole ? 1 : kMinUnits + a.lead;
     // no more CTAs than there can be shares of the line
     const int64_t segs = (((int64_t)c.n_tokens * a.G + R - 1) / R + c.n_rows) * c.Hkv;

@@ -50,6 +50,7 @@ constexpr int kThreads = 512;
 constexpr int kConvWarps = 7;
 constexpr int kConvThreads = 32 * kConvWarps;
 constexpr int kIssueWarp = 8;
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
 constexpr int kChunk = 128;                    // keys of a chunk
 constexpr int kRing = 4;                       // chunks whose scales are at hand
 constexpr uint32_t kTmemCols = 512;            // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512)
@@ -165,10 +166,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *tmem_holder;
+    // a warpgroup's warps all take the same one: the last two warpgroups hold both of the other roles
+    static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * 128, "no more than the block has");
+    static_assert(kIssueWarp == 8 && kIssueWarp + 1 + kConvWarps == kThreads / 32, "two warpgroups and two");
+    if (warp < 8) tc::regs_up<kSoftmaxRegs>();
+    else tc::regs_down<kOtherRegs>();
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
-        tc::regs_up<192>();
         const int h = warp / 4;
         const int tr = tid % 128;                                     // row of the tile, TMEM lane
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -473,7 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         }
     } else if (warp > kIssueWarp) {
         // ------------------------------------------------------------ codes to operands
-        tc::regs_down<64>();
         const int cw = warp - kIssueWarp - 1;
         // A block is the 512 bytes (kKeys keys) that a warp copies or converts at a time; the warps take every third.
         // lane -> (key, 16-byte chunk) so that eight lanes' 16-byte writes meet no bank twice
@@ -585,7 +589,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         cp_async_wait_all();
     } else {
         // ------------------------------------------------------------ products
-        tc::regs_down<64>();
         {
             constexpr uint32_t idS = tc::idesc_f16(128, 128, false), idO = tc::idesc_f16(128, D, true);
             int gc = 0, cnt0 = 0, cnt1 = 0, nq0 = 0, nq1 = 0;

@@ -10,9 +10,14 @@
 // but for a power of two (2^e of its largest element, put back on the scores;
 // elements below 2^-17 of the row's largest lose bits, less than 2^-25 of it
 // absolute), so no product is rounded; sums, maxima and l are fp32.  The weights
-// are rounded to fp16 (2^-11 relative, finer than the bf16 of the output).  b_j
-// is taken relative to the largest b so far, as m is for x, so weights stay
-// within fp16's range whatever the scales.
+// are rounded to fp16 (2^-11 relative, finer than the bf16 of the output).  To
+// keep them within its range b_j is taken relative to a reference of the warp's,
+// 2^6 times the first scale it meets, as long as all its scales lie between 2^-11
+// and 2 of that (a caller's usually do).  From the first that does not on (pages
+// of zeros beside others, an outlier, another quantiser's) each row keeps the
+// largest x_j log2 e + log2 b_j of the keys it sees as a reference of its own and
+// w_j is an exponential of its own, so that a page nobody attends, however large
+// its scale, takes no bits from the others.
 //
 // Layout: bound by streaming the codes from HBM.  A warp takes 32 keys at a
 // time through a ring of its own in shared memory (cp.async, 16 bytes a lane,
@@ -29,6 +34,8 @@
 // D = 128): 214 us, 5.7 TB/s; capped 238 us.  Three rows of 9k-180k int8 keys with a
 // distance bias (0.33 GB): 86 us.  Some 780 instructions a warp and tile keep half
 // of the issue slots busy, so what is left is latency and issue, not bytes alone.
+#include <type_traits>
+
 #include "cache_codes.cuh"
 #include "cache_plan.cuh"
 
@@ -59,7 +66,7 @@ struct Smem {
     alignas(16) float sc[kWarps][kStages][4];                  // K, K, V, V scales of the two 16-key halves
     int bad[kWarps][kStages];                                  // bit h: half h lies in a page that is not there
     float m[kWarps][16 * MT], l[kWarps][16 * MT];
-    float vref[kWarps];
+    float vr[kWarps][16 * MT];                                 // what O is relative to, beside 2^m
     PlanSmem<kThreads> plan;
     alignas(16) uint32_t qf[MT > 1 ? MT * (D / 16) * 128 : 4];  // query fragments (MT > 1; else in registers)
     static_assert(16 * MT * D * 4 <= kStages * kStageBytes, "the O buffer fits the rings");
@@ -226,7 +233,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
 
         float o[MT][NT][4];
         float m[2 * MT], l[2 * MT];
-        float vref = 1.17549435e-38f;
+        // O is relative to 2^m / inv_vref (a power of two; 0: no scale met yet) or, where inv_vref < 0, to 2^vr (of the
+        // row, in shared memory)
+        float inv_vref = 0.f;
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
             m[i] = -INFINITY;
@@ -358,52 +367,87 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
             }
 
             // ---- running maximum, weights
-            const float vnew = fmaxf(vref, fmaxf(vsc[0], vsc[1]));
-            const float vdown = vref / vnew;
-            const float vrel[2] = {vsc[0] / vnew, vsc[1] / vnew};
-            float alpha[2 * MT];
-            bool grew = vnew != vref;
-            vref = vnew;
-#pragma unroll
-            for (int r2 = 0; r2 < 2 * MT; ++r2) {
-                const int mt = r2 / 2, e0 = 2 * (r2 & 1);
-                float f[2], mx = -INFINITY;
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    f[hf] = slow ? 1.f : fac[r2] * ksc[hf] * kLog2e;
-                    const float top = fmaxf(fmaxf(s[mt][2 * hf][e0], s[mt][2 * hf][e0 + 1]),
-                                            fmaxf(s[mt][2 * hf + 1][e0], s[mt][2 * hf + 1][e0 + 1]));
-                    mx = fmaxf(mx, top * f[hf]);
+            float vrel[2] = {vsc[0] * inv_vref, vsc[1] * inv_vref};
+            const auto near = [](float x) { return __float_as_uint(x) - __float_as_uint(0x1p-11f) <= 12u << 23; };   // 2^-11 <= x <= 2
+            bool odd = false;
+            if (!(near(vrel[0]) && near(vrel[1]))) {
+                if (inv_vref == 0.f && (vsc[0] > 0.f || vsc[1] > 0.f)) {   // (of no scale yet)
+                    const float v = fminf(fmaxf(vsc[0] > 0.f ? vsc[0] : vsc[1], 0x1p-90f), 0x1p90f);
+                    inv_vref = 1.f / (64.f * __uint_as_float(__float_as_uint(v) & 0x7f800000u));
+                    vrel[0] = vsc[0] * inv_vref;
+                    vrel[1] = vsc[1] * inv_vref;
                 }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float m_new = fmaxf(m[r2], mx);
-                const float ref = m_new == -INFINITY ? 0.f : m_new;
-                alpha[r2] = exp2_fast(m[r2] - ref);      // 0 while nothing was seen
-                grew |= m_new != m[r2];
-                m[r2] = m_new;
-                const float bias = ref - kBias;
-                float sum = 0.f;
+                odd = (vsc[0] > 0.f && !near(vrel[0])) || (vsc[1] > 0.f && !near(vrel[1])) || inv_vref < 0.f;
+                if (odd && inv_vref > 0.f) {
+                    if (qc == 0)
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float p = exp2_fast(fmaf(s[mt][nt][e0 + e], f[nt / 2], -bias));
-                        sum += p;
-                        s[mt][nt][e0 + e] = p * vrel[nt / 2];
-                    }
-                l[r2] = l[r2] * alpha[r2] + sum;
+                        for (int r2 = 0; r2 < 2 * MT; ++r2) sm.vr[warp][qr + 8 * r2] = m[r2] - log2_fast(inv_vref);
+                    __syncwarp();
+                    inv_vref = -inv_vref;
+                }
             }
-            if (__any_sync(0xffffffffu, grew)) {
+            float alpha[2 * MT];
+            bool grew = false;
+            const auto weigh = [&](auto is_odd) {   // (two bodies: a branch for each row would hold their overlap back)
+                constexpr bool kOdd = decltype(is_odd)::value;
+                const float logv[2] = {kOdd ? log2_fast(vsc[0]) : 0.f, kOdd ? log2_fast(vsc[1]) : 0.f};
 #pragma unroll
                 for (int r2 = 0; r2 < 2 * MT; ++r2) {
-                    const float f = alpha[r2] * vdown;
+                    const int mt = r2 / 2, e0 = 2 * (r2 & 1);
+                    float f[2], mx = -INFINITY, tw = -INFINITY;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        f[hf] = slow ? 1.f : fac[r2] * ksc[hf] * kLog2e;
+                        const float top = fmaxf(fmaxf(s[mt][2 * hf][e0], s[mt][2 * hf][e0 + 1]),
+                                                fmaxf(s[mt][2 * hf + 1][e0], s[mt][2 * hf + 1][e0 + 1]));
+                        mx = fmaxf(mx, top * f[hf]);
+                        if constexpr (kOdd) tw = fmaxf(tw, top * f[hf] + logv[hf]);
+                    }
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float m_new = fmaxf(m[r2], mx);
+                    const float ref = m_new == -INFINITY ? 0.f : m_new;
+                    alpha[r2] = exp2_fast(m[r2] - ref);      // 0 while nothing was seen
+                    grew |= m_new != m[r2];
+                    m[r2] = m_new;
+                    const float bias = ref - kBias;
+                    float t_ref = 0.f, o_alpha = alpha[r2];
+                    if constexpr (kOdd) {
+                        tw = fmaxf(tw, __shfl_xor_sync(0xffffffffu, tw, 1));
+                        tw = fmaxf(tw, __shfl_xor_sync(0xffffffffu, tw, 2));
+                        const float t_old = sm.vr[warp][qr + 8 * r2], t_new = fmaxf(t_old, tw);
+                        t_ref = t_new == -INFINITY ? 0.f : t_new;
+                        o_alpha = exp2_fast(t_old - t_ref);
+                        grew |= t_new != t_old;
+                        __syncwarp();
+                        if (qc == 0) sm.vr[warp][qr + 8 * r2] = t_new;
+                        __syncwarp();
+                    }
+                    float sum = 0.f;
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = s[mt][nt][e0 + e];
+                            const float p = exp2_fast(fmaf(x, f[nt / 2], -bias));
+                            sum += p;
+                            if constexpr (kOdd) s[mt][nt][e0 + e] = exp2_fast(fmaf(x, f[nt / 2], logv[nt / 2] - t_ref + kBias));
+                            else s[mt][nt][e0 + e] = p * vrel[nt / 2];
+                        }
+                    l[r2] = l[r2] * alpha[r2] + sum;
+                    alpha[r2] = o_alpha;                     // (from here on O's)
+                }
+            };
+            if (!odd) weigh(std::false_type{});
+            else weigh(std::true_type{});
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int r2 = 0; r2 < 2 * MT; ++r2)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        o[r2 / 2][n][2 * (r2 & 1)] *= f;
-                        o[r2 / 2][n][2 * (r2 & 1) + 1] *= f;
+                        o[r2 / 2][n][2 * (r2 & 1)] *= alpha[r2];
+                        o[r2 / 2][n][2 * (r2 & 1) + 1] *= alpha[r2];
                     }
-                }
             }
 
             // ---- O += W V on the codes
@@ -461,6 +505,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
             if (qc == 0) {
                 sm.m[warp][rr] = m[r2];
                 sm.l[warp][rr] = t;
+                // (no scale passes 2^128, so neither does this)
+                sm.vr[warp][rr] = m[r2] == -INFINITY || inv_vref == 0.f ? 0.f
+                                  : inv_vref > 0.f ? 1.f / inv_vref : exp2f(fminf(sm.vr[warp][rr] - m[r2], 0x1.fffffep6f));
             }
             // lane (qr, qc) holds, for each n tile, dims of n index 2 qc and 2 qc + 1
 #pragma unroll
@@ -473,12 +520,12 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
                                     o[r2 / 2][n + 2][2 * (r2 & 1) + e], o[r2 / 2][n + 3][2 * (r2 & 1) + e]);
             }
         }
-        if (lane == 0) sm.vref[warp] = vref;
         __syncthreads();
         const bool all = cur.u == 0 && u1 == cur.units;   // the whole segment was this block's
         const int slot = cur.u == 0 ? 1 : 0;
         const float *obase = reinterpret_cast<const float *>(smem_raw);
-        // a thread a row: the warps' factors (over their m), and the row's sum
+        // a thread a row: the warps' factors, relative to the largest (in place of m), the factor that is left of all of
+        // them and the row's sum (in place of l): in this order no product leaves fp32's range where the result does not
         const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * R;
         auto out_row = [&](int ia) { return (int64_t)(row.t0 + ia / a.G) * a.Hq + cur.g * a.G + ia % a.G; };
         if (tid < R) {
@@ -492,9 +539,21 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
                 f[k] = exp2_fast(sm.m[k][tid] - ref);
                 lsum += sm.l[k][tid] * f[k];
             }
-            const float scale = !all ? 1.f : lsum == 0.f ? 0.f : 1.f / lsum;
+            float most = 0.f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) sm.m[k][tid] = f[k] * sm.vref[k] * scale;
+            for (int k = 0; k < kWarps; ++k) {
+                f[k] *= sm.vr[k][tid];
+                most = fmaxf(most, f[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) sm.m[k][tid] = most > 0.f ? f[k] / most : 0.f;
+            const bool huge = !all && most > 0x1p80f;   // (sums of such values would overflow: the part's mean instead)
+            sm.l[0][tid] = !all && !huge ? 1.f : lsum == 0.f ? 0.f : 1.f / lsum;
+            sm.l[1][tid] = most;
+            if (huge) {
+                mm += log2f(lsum);
+                lsum = 1.f;
+            }
             const int ia = cur.t * R + tid;
             if (ia < row.n * a.G) {
                 if (all) a.lse[out_row(ia)] = lsum == 0.f ? -INFINITY : (ref - kBias + log2f(lsum)) * kLn2;
@@ -515,6 +574,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) cache_attend_kernel
                 x[0] += y0.x * fv; x[1] += y0.y * fv; x[2] += y0.z * fv; x[3] += y0.w * fv;
                 x[4] += y1.x * fv; x[5] += y1.y * fv; x[6] += y1.z * fv; x[7] += y1.w * fv;
             }
+            const float scale = sm.l[0][rr], most = sm.l[1][rr];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = x[e] * scale * most;
             if (all) {
                 uint4 pk;
                 __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&pk);

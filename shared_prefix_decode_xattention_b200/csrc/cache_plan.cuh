@@ -272,6 +272,12 @@ __device__ __forceinline__ float exp2_fast(float x) {   // one MUFU op; tiny res
     return y;
 }
 
+__device__ __forceinline__ float log2_fast(float x) {   // one MUFU op and the scaling of tiny arguments
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // c * tanh(y) with tanh from one exponential and one reciprocal: 1 - 2 / (1 + e^2y).
 // Its error is a few 2^-24 absolute, which is what counts in an exponent; the
 // hardware's own tanh (about 2^-11) would put 2 % on a weight at a cap of 50.

@@ -7,8 +7,12 @@
 // the V scale joins the score: t_j = x_j log2 e + log2 b_j is the exponent of
 // the weight w_j = b_j p_j, one lazily raised reference M per row bounds it
 // (raised when a chunk passes it by more than 2^8), and l sums w_j / b_j, so
-// neither scale costs an instruction per score.  Rounded are the weights (fp16)
-// and the output (bf16); all else is fp32.
+// neither scale costs an instruction per score.  That is sound while the V scales
+// lie between 2^-60 and 2^30: beyond, a b_j far from the others would push w_j or
+// l out of fp32's range.  From a segment's first chunk with such a scale on (pages
+// of zeros have the smallest) l is summed from the scores themselves, 2^(x_j log2 e - P)
+// with a reference P of its own.  Rounded are the weights (fp16) and the output
+// (bf16); all else is fp32.
 //
 // One CTA per SM, persistent over its share of the work line (cache_plan.cuh);
 // a tile is 256 query rows, two products of 128 rows; 16 warps:
@@ -54,12 +58,15 @@ constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
 constexpr int kChunk = 128;                    // keys of a chunk
 constexpr int kRing = 4;                       // chunks whose scales are at hand
 constexpr uint32_t kTmemCols = 512;            // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512)
-constexpr float kMinLogV = -100.f;             // log2 of the smallest V scale told from 0
+constexpr float kZeroLogV = -150.f;            // log2 of a V scale of 0, as good as it: 448 * 2^-150 is 0 in bf16
+constexpr float kLowLogV = -60.f, kHighLogV = 30.f;   // scales for which l may be summed from the weights
+constexpr int kSick = 256, kFar = 512;         // of Scales::bad: a scale is NaN; the segment has met scales past those
 
 struct Scales {
-    float2 k[8];                // by 16 keys: K scale, log2 V scale
-    float iv[8];                // 1 / V scale
-    int bad;                    // bit g: group g lies in a page that is not there; bit 8: a scale is NaN (the slow way)
+    float2 k[8];                // by 16 keys: K scale, log2 V scale (0 where far)
+    float iv[8];                // 1 / V scale (0 where far)
+    float lv[8];                // log2 V scale
+    int bad;                    // bit g: group g lies in a page that is not there; kSick, kFar (all take the slow way)
     int pad[3];
 };
 
@@ -72,8 +79,10 @@ struct Lay {
     static constexpr uint32_t v = 4 * kTile;
     static constexpr uint32_t raw = 6 * kTile;                // codes of the next K and V chunk (first the plan's scratch)
     static constexpr uint32_t sc = raw + 2 * kChunk * D;
-    static constexpr uint32_t x = sc + kRing * sizeof(Scales);   // [128] (M, l) of a narrow segment's second half
-    static constexpr uint32_t unit = x + 1024;
+    static constexpr uint32_t p = sc + kRing * sizeof(Scales);   // [256] P of the rows of a segment past the scales' limits
+    static constexpr uint32_t unit = p + 1024;
+    static constexpr uint32_t x = kTile;                      // [128] (M, l) of a narrow segment's second half: it has no
+                                                              // second Q tile
     static constexpr uint32_t bar = unit + 64;
     static constexpr uint32_t misc = bar + 256;
     static constexpr uint32_t total = misc + 16 + 1024;       // with room to align the window
@@ -112,6 +121,53 @@ __device__ __forceinline__ Seg segment(const AttendArgs &a, const Parts &w, cons
     s.rows = min(R, s.row.n * a.G - cur.t * R);
     s.narrow = s.rows <= 128;
     return s;
+}
+
+// A chunk past the scales' limits: its scores, log2 units without the V scales, into l (relative to 2^far_p from then on,
+// to 2^M before), and the V scales onto them.  Called by whole warps; not inlined, as with far_mean, since the loop around
+// it is rarely gone through and its registers are all taken (inlined: packed chunks 217 us, 214 so).
+__device__ __noinline__ float far_sum(uint32_t ts, const Scales &sc, float &far_p, float M, float l) {
+    float P = far_p == INFINITY ? M : far_p;
+#pragma unroll 1
+    for (int p = 0; p < 4; ++p) {
+        float x[32], top = -INFINITY, sum = 0.f;
+        tc::ld32(ts + 32u * p, x);
+        tc::wait_ld_into(x);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e]);
+        const float up_to = fmaxf(P, top), ref = up_to == -INFINITY ? 0.f : up_to;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            sum += exp2_fast(x[e] - ref + kTcBias);
+            x[e] = x[e] == -INFINITY ? x[e] : x[e] + sc.lv[2 * p + e / 16];
+        }
+        l = l * exp2_fast(P - ref) + sum;
+        P = up_to;
+        __syncwarp();
+        tc::st32(ts + 32u * p, reinterpret_cast<const uint32_t *>(x));
+    }
+    tc::wait_st();
+    far_p = fminf(P, 0x1.fffffep127f);   // (infinite stands for no such chunk, in every thread alike)
+    return l;
+}
+
+// The result of such a segment in the usual form: O the mean, l = 1, relative to 2^M.
+template <int D>
+__device__ __noinline__ float2 far_mean(uint32_t to, float P, float M, float l) {
+    tc::fence_after();
+    const float mean = l == 0.f ? 0.f : 1.f / l, f = M == -INFINITY ? 0.f : exp2f(M - P);
+#pragma unroll 1
+    for (int p = 0; p < D / 32; ++p) {
+        float o[32];
+        tc::ld32(to + 32u * p, o);
+        tc::wait_ld_into(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = o[e] * mean * f;
+        __syncwarp();
+        tc::st32(to + 32u * p, reinterpret_cast<const uint32_t *>(o));
+    }
+    tc::wait_st();
+    return make_float2(P + log2f(l), l == 0.f ? 0.f : 1.f);
 }
 
 template <int D, int FMT>
@@ -250,7 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             const int lo_max = __reduce_max_sync(0xffffffffu, valid ? vis.lo : 0);
             const int hi_min = __reduce_min_sync(0xffffffffu, vis.hi);
 
+            // l is relative to 2^M, as O is, and from a chunk marked kFar on to 2^P, P in shared memory (infinite before)
             float M = -INFINITY, l = 0.f;
+            float &far_p = *reinterpret_cast<float *>(base + L::p + 4 * (tid & 255));
+            far_p = INFINITY;
             for (int i = 0; i < n; ++i) {
                 const int ch = s.chunk_of(h, i), gi = gc + ch;
                 ok = mbar_wait(bar(B_SC + gi % kRing), (gi / kRing) & 1, abort) &&
@@ -314,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                         tc::st32(ts + 32u * p, reinterpret_cast<const uint32_t *>(x));
                     }
                     tc::wait_st();
+                    if (sc.bad & kFar) l = far_sum(ts, sc, far_p, M, l);
                 }
                 float x[128];
 #pragma unroll
@@ -338,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 if (raise) {
                     alpha = exp2_fast(M - top);
                     M = top;
-                    l *= alpha;
+                    if (!(sc.bad & kFar)) l *= alpha;
                 }
                 if (i > 0 && __any_sync(0xffffffffu, raise)) {   // O_h holds every product so far: S_h waited for them
 #pragma unroll 1
@@ -383,6 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             if (ok && n > 0) ok = mbar_wait(bar(B_PVDONE + h), (cnt + n - 1) & 1, abort);
             cnt += n;
             gc += s.chunks;
+            if (ok && far_p != INFINITY) {   // (of whole warps)
+                const float2 ml = far_mean<D>(to, far_p, M, l);
+                M = ml.x;
+                l = ml.y;
+            }
             bool fold = false;   // a narrow segment's second half is folded in
             float a0 = 1.f, a1 = 0.f;
             if (ok && s.narrow && s.chunks > 1) {
@@ -507,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 const int key = s.kb0 + ch * kChunk + 16 * (lane & 7);
                 return id < 0 ? -1 : (id * c.Hkv + cur.g) * (c.page / 16) + (key & (c.page - 1)) / 16;
             };
+            int met = 0;   // kFar: a chunk of the segment had a scale past the limits
             // a thread's codes wait in shared memory of its own (16 bytes of each block)
             const uint32_t raw = L::raw + 16u * lane, raw_v = raw + kChunk * D;
             auto load = [&](const uint8_t *src, uint32_t to, int ch, int block) {
@@ -557,15 +623,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                         ks = clean_scale(c.ks[at_s]);
                         vs = clean_scale(c.vs[at_s]);
                     }
-                    const float lv = vs != vs ? vs : fmaxf(log2f(vs), kMinLogV);
+                    const float lv = ids < 0 ? 0.f : vs != vs ? vs : fmaxf(log2f(vs), kZeroLogV);
+                    if (__any_sync(0xffffffffu, lv < kLowLogV || lv > kHighLogV)) met = kFar;
                     Scales &sc = ring[gi % kRing];
                     const uint32_t gone = __ballot_sync(0xffffffffu, ids == -1) & 255u;
                     const uint32_t sick = __ballot_sync(0xffffffffu, vs != vs || ks != ks) & 255u;
                     if (lane < 8) {
-                        sc.k[lane] = make_float2(ks, lv);
-                        sc.iv[lane] = exp2f(-lv);
+                        sc.k[lane] = make_float2(ks, met ? 0.f : lv);
+                        sc.iv[lane] = met ? 0.f : exp2f(-lv);
+                        sc.lv[lane] = lv;
                     }
-                    if (lane == 0) sc.bad = (int)gone | (sick ? 256 : 0);
+                    if (lane == 0) sc.bad = (int)gone | (sick ? kSick : 0) | met;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_SC + gi % kRing));
                 }

@@ -122,3 +122,47 @@ def test_few_rows_hidden_page(window, n, G, d, fmt):
 def test_few_rows_faint_page(n, G, d, fmt):
     """A bias leaves the outlier's page a weight that its scale makes up for, or next to none."""
     row_case("outlier first", n, G, d, fmt, 250, 2, slopes=[0.2, 0.25, 0.17, 1.0, 0.21, 0.15, 0.22, 0.3][: HKV * G])
+
+
+MANY = [(100, 4, 128, "e4m3"), (100, 1, 64, "int8"), (40, 3, 128, "int8"), (300, 2, 64, "e4m3")]     # 256-row tiles
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,G,d,fmt", MANY)
+def test_many_rows(kind, n, G, d, fmt):
+    row_case(kind, n, G, d, fmt, 320, 2)
+    row_case(kind, n, G, d, fmt, 320, 2, seed=1, mask="full", softcap=20.0)
+    row_case(kind, n, G, d, fmt, 1500, 2, seed=2, page=64)                # cut among blocks
+    row_case(kind, n, G, d, fmt, 310, 2, seed=3, slopes=[0.3, 0.1, 0.2, 0.25, 0.4, 0.15, 0.22, 0.35][: HKV * G])
+
+
+@pytest.mark.parametrize("n,G,d,fmt", MANY)
+def test_many_rows_hidden_page(n, G, d, fmt):
+    first = (np.arange(n) * 7 % 80).astype(np.int32)            # of the outliers' 32 keys queries see all, some or none
+    row_case("outlier first", n, G, d, fmt, 320, 2, first=first)
+    row_case("outlier first", n, G, d, fmt, 1320, 2, first=first, mask="full")
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_lse_of_long_heads_of_zeros(n):
+    """V all zero, as a store leaves it, in 200 rows of the same 40000 keys whose first score lower than the rest: the
+    sum stays finite, also where a block takes all keys of a row.  Every score is 64 ones times a code and a scale:
+    exact but for the scale's three roundings, so the sum is known."""
+    L, page, d, rows = 40000, 128, 64, 200
+    cache = random_cache(np.random.default_rng(0), 320, HKV, page, d, "int8")
+    cache["k"][:] = 64
+    cache["v"][:] = 0
+    cache["vs"][:] = 2.0 ** -126
+    cache["ks"][:] = np.float32(4.7 / 512)
+    cache["ks"][5] = 0.0
+    ids = np.r_[5, np.delete(np.arange(320), 5)][None, : -(-L // page)]
+    pc = to_device(cache)
+    q = torch.ones((rows * n, HKV, d), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda"), torch.full(q.shape[:2], 7.0, device="cuda")
+    pc.attend(i32(ids.repeat(rows, 0)), i32([L] * rows), i32(np.arange(rows + 1) * n), q, out, lse, max_q=n, mask="full")
+    assert pc.device_status() == 0
+    score = 512 * float(np.float32(4.7 / 512))
+    want = score + np.log(L - page + page * np.exp(-score))
+    # (the sum of at most 40000 terms of one sign, in any order: each addition 2^-24 of it; hundreds in a chain)
+    assert (lse.double() - want).abs().max().item() <= 2.0 ** -24 * (16 * want + 16 * score + 1000)
+    assert not out.any()

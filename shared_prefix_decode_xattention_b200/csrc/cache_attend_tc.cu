@@ -98,6 +98,13 @@ __device__ __forceinline__ uint32_t sw128(int row, int c) {
     return (uint32_t)(c >> 3) * Lay<D>::kHalf + (uint32_t)row * 128u + (uint32_t)(((c & 7) ^ (row & 7)) << 4);
 }
 
+// Bounded waits of a whole warp, with one verdict: a lane that gave up alone would leave the others in instructions that
+// take all 32.  (In the loops over chunks the vote stands beside slower work: right after the waits it cost 4 % of the
+// packed chunks' time, there 1.5 %.)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 // A segment as every role sees it.
 struct Seg {
     RowSpan row;
@@ -312,9 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             far_p = INFINITY;
             for (int i = 0; i < n; ++i) {
                 const int ch = s.chunk_of(h, i), gi = gc + ch;
-                ok = mbar_wait(bar(B_SC + gi % kRing), (gi / kRing) & 1, abort) &&
-                     mbar_wait(bar(B_SFULL + h), (cnt + i) & 1, abort);
-                if (!ok) break;
+                const bool here = mbar_wait(bar(B_SC + gi % kRing), (gi / kRing) & 1, abort) &&
+                                  mbar_wait(bar(B_SFULL + h), (cnt + i) & 1, abort);
                 tc::fence_after();
                 const Scales &sc = ring[gi % kRing];
                 const int key0 = s.kb0 + ch * kChunk;
@@ -378,8 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 float x[128];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) tc::ld32(ts + 32u * p, x + 32 * p);
+                ok = __all_sync(0xffffffffu, here);   // (beside the loads; until here a warp that gave up reads what is there)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) tc::wait_ld_into(x + 32 * p);
+                if (!ok) break;
                 // t = fo.x f1 x + fo.y is a weight's exponent (x itself after the slow way)
                 const float2 *fo = slow ? unit : sc.k;
                 const float f1 = slow ? 1.f : f0;
@@ -440,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 mbar_arrive(bar(B_PFULL + h));
             }
             // ---- the segment's result
-            if (ok && n > 0) ok = mbar_wait(bar(B_PVDONE + h), (cnt + n - 1) & 1, abort);
+            if (ok && n > 0) ok = warp_wait(bar(B_PVDONE + h), (cnt + n - 1) & 1, abort);
             cnt += n;
             gc += s.chunks;
             if (ok && far_p != INFINITY) {   // (of whole warps)
@@ -455,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                     tc::fence_before();
                     xch[tr] = make_float2(M, l);
                     mbar_arrive(bar(B_XCH));
-                    ok = mbar_wait(bar(B_XDONE), nx & 1, abort);   // O_1 and xch are read
+                    ok = warp_wait(bar(B_XDONE), nx & 1, abort);   // O_1 and xch are read
                 } else {
-                    ok = mbar_wait(bar(B_XCH), nx & 1, abort);
+                    ok = warp_wait(bar(B_XCH), nx & 1, abort);
                     const float2 y = xch[tr];
                     const float m = fmaxf(M, y.x), ref = m == -INFINITY ? 0.f : m;
                     a0 = exp2_fast(M - ref);
@@ -614,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 const int ids2 = next;
                 next = ids_of(ch + 2);
                 if (gi >= 2) ok = mbar_wait(bar(B_KEMPTY + st), ((gi >> 1) - 1) & 1, abort);
-                if (!ok) break;
                 // (S of chunk gi - 2 is complete, so the softmax is done with the scales of chunk gi - 4)
                 if (cw == 0) {   // the chunk's scales
                     float ks = 0.f, vs = 0.f;
@@ -642,13 +649,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 mbar_arrive(bar(B_KFULL + st));
                 block = block_of(ch + 1, ids2);
                 load(c.k, raw, ch + 1, block);
-                if (gi >= 2) ok = mbar_wait(bar(B_VEMPTY + st), ((gi >> 1) - 1) & 1, abort);
-                if (!ok) break;
+                if (gi >= 2) ok = ok && mbar_wait(bar(B_VEMPTY + st), ((gi >> 1) - 1) & 1, abort);
                 cp_async_wait_group<1>();
                 put(L::v + st * L::kTile, raw_v);
                 mbar_arrive(bar(B_VFULL + st));
                 load(c.v, raw_v, ch + 1, block);
                 ids = ids2;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
             }
             gc += s.chunks;
             left -= s.u1 - cur.u;

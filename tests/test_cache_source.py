@@ -18,3 +18,17 @@ def test_registers_are_exchanged_by_whole_warpgroups():
     assert len(up) == 1 and len(down) == 1
     assert max(up[0], down[0]) < src.index("else if (warp > kIssueWarp)")
     assert re.search(r"if \(warp < 8\) tc::regs_up<\w+>\(\);\s*else tc::regs_down<\w+>\(\);", src)
+
+
+def test_waits_of_whole_warps_have_one_verdict():
+    """Softmax and conversion warps go on to instructions of all 32 lanes: no lane leaves a loop on its own wait's result,
+    but all do by a vote on it."""
+    src = source("cache_attend_tc.cu")
+    roles = src[src.index("if (warp < 8) {\n"):src.index("idS = tc::idesc")]
+    exits = [m.start() for m in re.finditer(r"if \(!ok\) break;", roles)]
+    assert len(exits) == 3                          # a chunk's softmax, a segment's end, a chunk's conversion
+    for at in exits:
+        last = list(re.finditer(r"ok = (\w+)\(", roles[:at]))[-1]
+        assert last.group(1) in ("warp_wait", "__all_sync"), roles[last.start():at]
+    lane = [m.group(0) for m in re.finditer(r"[^;{}]*\bmbar_wait\(", roles)]
+    assert len(lane) == 3                           # (put to those votes: the scores' and the two operand buffers')

@@ -44,7 +44,10 @@
  * XGR_DEV_CAPACITY) set bits in the caller's status word (d_status, int32,
  * never cleared by these calls), and the faulty element is skipped: a key in a
  * page that is not there is not attended, a token without a page is not
- * stored, a row whose d_cu or length is at fault has no tokens.
+ * stored, a row whose length is at fault has no tokens.  Where d_cu is out of
+ * order or past n_tokens anywhere, no row of an xgr_cache_attend has tokens, and
+ * rows of an xgr_cache_store may be left out, each whole (XGR_DEV_INDEX in any
+ * case).
  * XGR_DEV_TIMEOUT, as in xgr.h: a bounded wait inside xgr_cache_attend gave up.
  * The workspace of a call (d_ws, 256-byte aligned, at least the bytes its
  * _bytes function gives) needs no initial contents and holds nothing between

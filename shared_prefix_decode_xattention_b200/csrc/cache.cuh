@@ -45,6 +45,21 @@ __device__ __forceinline__ RowSpan row_span(const CacheArgs &a, int r, int max_n
     return s;
 }
 
+// d_cu[i] and d_cu[i + 1], read here and now: their checks may stand behind other work.  (Rows are found by a search in
+// d_cu, which misses some and finds others twice where it does not ascend.)
+struct CuPair {
+    int a, b;
+};
+__device__ __forceinline__ CuPair cu_pair(const CacheArgs &c, int i) {
+    CuPair p;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(p.a) : "l"(c.cu + i));
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(p.b) : "l"(c.cu + i + 1));
+    return p;
+}
+__device__ __forceinline__ bool out_of_order(const CacheArgs &c, const CuPair &p) {
+    return p.a < 0 || p.a > p.b || p.b > c.n_tokens;
+}
+
 // Validation and the launches' arguments (cache_api.cu).
 inline bool al(const void *p, size_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 

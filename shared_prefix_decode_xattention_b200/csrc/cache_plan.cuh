@@ -147,9 +147,9 @@ struct PlanSmem {
     Cursor first;
 };
 
-// Exclusive sum over the block's threads; the sum of all is sm.base[T / 32].
+// Exclusive sum over the block's threads; the sum of all is sm.base[T / 32].  `any`: whether it was set in any thread.
 template <int T>
-__device__ __forceinline__ int64_t plan_scan(PlanSmem<T> &sm, int64_t v) {
+__device__ __forceinline__ int64_t plan_scan(PlanSmem<T> &sm, int64_t v, bool &any) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     int64_t x = v;
 #pragma unroll
@@ -157,7 +157,7 @@ __device__ __forceinline__ int64_t plan_scan(PlanSmem<T> &sm, int64_t v) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    __syncthreads();
+    any = __syncthreads_or(any);
     if (lane == 31) sm.base[warp + 1] = x;
     if (threadIdx.x == 0) sm.base[0] = 0;
     __syncthreads();
@@ -174,15 +174,19 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_u
                                            const PlanOut &p, U &w, Cursor &cur, int64_t &begin, int64_t &end) {
     const int64_t slots = tile_slots(a, R), spt = (slots + T - 1) / T;
     const int64_t s0 = min(threadIdx.x * spt, slots), s1 = min(s0 + spt, slots);
+    const CuPair pair = cu_pair(a.c, min((int)threadIdx.x, a.c.n_rows - 1));
+    bool bad = false;
+    for (int i = threadIdx.x + T; i < a.c.n_rows; i += T) bad |= out_of_order(a.c, cu_pair(a.c, i));
     int units = 0, r = 0;
     int64_t t = 0;
     KeyRange k{0, 0};
     if constexpr (U::kParts) {   // chunks and segments in all
         int64_t both = 0;
+        bool unused = false;
         if (!a.whole)
             for (int64_t s = s0; s < s1; ++s)
                 if (slot_keys(a, R, s, r, t, k)) both += ((int64_t)range_chunks(k) << 24) + 1;
-        plan_scan<T>(sm, both);
+        plan_scan<T>(sm, both, unused);
         const int64_t segs = (sm.base[T / 32] & 0xffffff) * a.c.Hkv, chunks = (sm.base[T / 32] >> 24) * a.c.Hkv;
         const bool few = segs > 0 && segs * 2 <= gridDim.x && chunks < 0x7fffffff;
         if (threadIdx.x == 0) {
@@ -198,8 +202,10 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_u
         if (slot_keys(a, R, s, r, t, k)) units = range_units(a, w, k);
         mine += (int64_t)units * a.c.Hkv;
     }
-    const int64_t from = plan_scan<T>(sm, mine);     // first unit of this thread's slots
-    const int64_t total = sm.base[T / 32];
+    bad |= out_of_order(a.c, pair);
+    const int64_t from = plan_scan<T>(sm, mine, bad);     // first unit of this thread's slots
+    if (bad) mine = 0;                                // (of every block: there is no work)
+    const int64_t total = bad ? 0 : sm.base[T / 32];
     const int64_t per = max((int64_t)min_units, (total + gridDim.x - 1) / gridDim.x);
     // the block's two edges, each found by the thread whose slots hold it
 #pragma unroll 1
@@ -233,6 +239,7 @@ __device__ __forceinline__ bool plan_begin(const AttendArgs &a, int R, int min_u
     } else {
         cur = Cursor{0, 0, 0, 0, 0};
     }
+    if (threadIdx.x == 0 && bad) set_status(a.c.status, XGR_DEV_INDEX);
     if (threadIdx.x == 0 && p.first) p.first[blockIdx.x] = cur;
     return begin < end;
 }

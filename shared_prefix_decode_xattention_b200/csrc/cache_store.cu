@@ -81,17 +81,26 @@ __global__ void __launch_bounds__(kThreads) cache_store_kernel(StoreArgs a, int 
     const int64_t unit = (int64_t)blockIdx.x * kGroups + group;
     const int slot = (int)(unit / c.Hkv), g = (int)(unit % c.Hkv);
     const bool v_side = blockIdx.y != 0;
+    if (!v_side && blockIdx.x <= c.n_rows / kThreads) {   // (there are more threads than rows)
+        const int i = blockIdx.x * kThreads + threadIdx.x;
+        if (i < c.n_rows && out_of_order(c, cu_pair(c, i))) set_status(c.status, XGR_DEV_INDEX);
+    }
     if (slot >= n_slots) return;
 
     // the row of this slot: slots are the rows themselves when no row has two
     // tokens, else found among the rows' slot bases
-    int r = slot, j = 0;
+    int r = slot, j = 0, below = 0, above = 0x7fffffff;   // (the largest base passed on the way that is below, the least above)
     if (a.max_n > 1) {
         int lo = 0, hi = c.n_rows - 1;
         while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (slot_base(c, mid) <= slot) lo = mid;
-            else hi = mid - 1;
+            const int mid = (lo + hi + 1) / 2, base = slot_base(c, mid);
+            if (base <= slot) {
+                lo = mid;
+                below = max(below, base);
+            } else {
+                hi = mid - 1;
+                above = min(above, base);
+            }
         }
         r = lo;
         j = slot - slot_base(c, r);
@@ -99,6 +108,8 @@ __global__ void __launch_bounds__(kThreads) cache_store_kernel(StoreArgs a, int 
     }
     const RowSpan row = row_span(c, r, a.max_n);
     if (row.n == 0) return;
+    // where d_cu is out of order: the search for the row's other slots takes the same way, or the row is left out whole
+    if (below > slot - j || above < ((row.t0 + row.n) >> c.page_shift) + 2 * (r + 1)) return;
     const int start = row.len - row.n;
     const int p = (start >> c.page_shift) + j;
     if (p > (row.len - 1) >> c.page_shift) return;

@@ -27,7 +27,8 @@
  * d_cu[n_rows] <= n_tokens; tokens behind d_cu[n_rows] belong to no row and
  * are neither read nor written).  They are the last of their row: token i of
  * n stands at position len - n + i, d_len counting them already.  A row may
- * have none.
+ * have none.  (Beams over a prompt, XGR_ATTN_FULL, are none of its tokens, and
+ * may outnumber them.)
  *
  * The order of a decode step: xgr_cache_fork (the rows' new parents, and pages
  * for the tokens to come), xgr_cache_store, xgr_cache_attend, a selection.
@@ -39,9 +40,9 @@
  * allocation.  Every call runs on the current device, which must be the
  * buffers'.  Faults found on the device (a page id outside [0, n_pages), a
  * length outside [0, max_pages * page_size], d_cu out of order or past
- * n_tokens, a row with more tokens than its length: XGR_DEV_INDEX; no free
- * page, a row longer than max_pages or with more tokens than max_n / max_q:
- * XGR_DEV_CAPACITY) set bits in the caller's status word (d_status, int32,
+ * n_tokens, a row with more tokens than its length but under XGR_ATTN_FULL:
+ * XGR_DEV_INDEX; no free page, a row longer than max_pages or with more tokens
+ * than max_n / max_q: XGR_DEV_CAPACITY) set bits in the caller's status word (d_status, int32,
  * never cleared by these calls), and the faulty element is skipped: a key in a
  * page that is not there is not attended, a token without a page is not
  * stored, a row whose length is at fault has no tokens.  Where d_cu is out of
@@ -117,7 +118,9 @@ typedef struct {
  * out = sum_j softmax(x)_j v_j; LSE = ln sum_j exp(x_j).
  * max_q: no row has more tokens than this (a row that does is skipped, and
  * XGR_DEV_CAPACITY set).  The beams of a request over its shared prompt are
- * one row with a token for each beam and XGR_ATTN_FULL.
+ * one row with a token for each beam and XGR_ATTN_FULL, as many as there are;
+ * slopes and window go by position under this mask too, where query i of n
+ * stands at len - n + i (below 0 where n > len), not all beams at the end.
  * n_q_heads: a multiple of n_kv_heads.  Contents behind a row's length are
  * never used, whatever bits are there. */
 xgr_status xgr_cache_attend_bytes(const xgr_cache *cache, int32_t n_q_heads, int32_t n_rows,

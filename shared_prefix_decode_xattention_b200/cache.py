@@ -154,8 +154,9 @@ class PagedCache:
                workspace=None):
         """Attention of packed query tokens q [T][Hq][D] (bf16) over the rows' pages into out
         [T][Hq][D] (bf16) and lse [T][Hq] (fp32); cu int32 [n_rows + 1].  mask: "full", "causal",
-        or "prefix" (causal beside a bidirectional prefix of prefix[r] tokens).  See
-        xgr_cache_attend."""
+        or "prefix" (causal beside a bidirectional prefix of prefix[r] tokens).  The beams of a
+        request over its prompt are one row under "full", however many (without slopes and window,
+        which go by position).  See xgr_cache_attend."""
         self._run(self._attend, table, length, cu, q, out, lse, max_q, scale, softcap, mask, window, slopes,
                   prefix, first, stream, workspace)
 

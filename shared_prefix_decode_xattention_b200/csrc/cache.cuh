@@ -25,6 +25,7 @@ struct CacheArgs {
     int32_t *status;
     int n_pages, page, page_shift, Hkv, D, fmt;
     int n_rows, max_pages, n_tokens;
+    int beams;                   // 1: a row may have more tokens than its length (beams over a prompt)
 };
 
 // A row's new tokens [t0, t0 + n) and its length; n = 0 and len = 0 where they do not fit together.
@@ -36,7 +37,7 @@ __device__ __forceinline__ RowSpan row_span(const CacheArgs &a, int r, int max_n
     const int t0 = a.cu[r], t1 = a.cu[r + 1], len = a.len[r];
     RowSpan s{t0, t1 - t0, len};
     const bool bad = t0 < 0 || t1 < t0 || t1 > a.n_tokens || len < 0 ||
-                     len > (int64_t)a.max_pages * a.page || t1 - t0 > len;
+                     len > (int64_t)a.max_pages * a.page || (t1 - t0 > len && !a.beams);
     if (bad || s.n > max_n) {
         set_status(a.status, bad ? XGR_DEV_INDEX : XGR_DEV_CAPACITY);
         s.n = 0;

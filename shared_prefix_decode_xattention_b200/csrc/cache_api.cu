@@ -119,6 +119,7 @@ extern "C" xgr_status xgr_cache_attend(const xgr_cache *cache, const xgr_cache_r
     a.scale = opts->scale > 0.f ? opts->scale : 1.f / std::sqrt((float)cache->head_dim);
     a.softcap = opts->softcap;
     a.causal = opts->mask == XGR_ATTN_CAUSAL;
+    a.c.beams = !a.causal;
     a.window = opts->window;
     a.slopes = opts->d_slopes;
     a.prefix = opts->d_prefix;

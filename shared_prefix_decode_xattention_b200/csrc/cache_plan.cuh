@@ -60,8 +60,10 @@ __device__ __forceinline__ int64_t tile_slots(const AttendArgs &a, int R) {
     return ((int64_t)a.c.n_tokens * a.G >> (31 - __clz(R))) + a.c.n_rows;
 }
 
-// The keys [lo, hi) that some query of tile t of a row with span s may see.
+// First key of the window of a query at pos (below 0 where beams outnumber the row's keys).
+__device__ __forceinline__ int window_lo(const AttendArgs &a, int pos) { return pos >= a.window ? pos - a.window + 1 : 0; }
 
+// The keys [lo, hi) that some query of tile t of a row with span s may see.
 __device__ __forceinline__ KeyRange tile_keys(const AttendArgs &a, const RowSpan &s, int r, int R, int t) {
     KeyRange k{0, s.len};
     const int i0 = t * R / a.G, i1 = (min((t + 1) * R, s.n * a.G) - 1) / a.G;   // its tokens
@@ -70,7 +72,7 @@ __device__ __forceinline__ KeyRange tile_keys(const AttendArgs &a, const RowSpan
         k.hi = p0 + i1 + 1;
         if (a.prefix) k.hi = max(k.hi, min(a.prefix[r], s.len));
     }
-    if (a.window > 0) k.lo = max(0, p0 + i0 - a.window + 1);
+    if (a.window > 0) k.lo = window_lo(a, p0 + i0);
     if (a.first) k.lo = max(k.lo, a.tile_lo[tile_slot(a, r, R) + t]);
     return k;
 }
@@ -252,7 +254,7 @@ __device__ __forceinline__ KeyRange query_keys(const AttendArgs &a, const RowSpa
         k.hi = pos + 1;
         if (a.prefix) k.hi = max(k.hi, min(a.prefix[r], s.len));
     }
-    if (a.window > 0) k.lo = max(0, pos - a.window + 1);
+    if (a.window > 0) k.lo = window_lo(a, pos);
     if (a.first) k.lo = max(k.lo, a.first[s.t0 + i]);
     return k;
 }

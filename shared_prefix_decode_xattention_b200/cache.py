@@ -6,8 +6,9 @@ The order of a decode step: ``fork`` (the rows' new parents, pages for the
 tokens to come), ``store``, ``attend``, a selection.
 
 Streams: a call runs on ``stream``, or on torch's current stream of the cache's
-device.  Each stream has a workspace of its own, so calls on two streams may
-overlap.  It is made by the first call that needs it and never freed before the
+device; the tensors it is given have to be ready there.  Each stream has a
+workspace of its own, so calls on two streams may overlap.  It is made by the
+first call that needs it, from that stream's memory, and never freed before the
 PagedCache.  A captured graph keeps using the workspace of the stream it was
 captured on; a call under capture that would have to make one raises.  So either
 make the call once before the capture, on the capturing stream, or give the
@@ -50,7 +51,10 @@ class PagedCache:
                                 self.n_pages, self.page_size, self.n_kv_heads, self.head_dim,
                                 fmt[k.dtype])
         xgr.xgr_cache_compact_bytes(self._c)      # refuses shapes the library does not take
+        if torch.cuda.is_current_stream_capturing():
+            _bad("PagedCache", "made under a capture: make it before", xgr.XGR_ERR_STATE)
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        torch.cuda.current_stream(self._index).synchronize()     # calls on any stream may set bits of it
         self._d_status = self._status.data_ptr()
         self._ws = {}                             # stream handle -> its workspace (tensor, bytes, address)
         self._old = []                            # outgrown workspaces: a captured graph may use them
@@ -117,13 +121,16 @@ class PagedCache:
         ws = self._ws.get(stream)
         if ws is None or ws[1] < need:
             torch = self._torch
-            if torch.cuda.is_current_stream_capturing():
-                _bad(fn, "no workspace of this size on the capturing stream yet: make the call once on it "
-                         "before the capture, or pass workspace", xgr.XGR_ERR_STATE)
-            if ws is not None:
-                self._old.append(ws[0])
-                need = max(need, 2 * ws[1])
-            t = torch.empty(need, dtype=torch.uint8, device=self.device)
+            own = (torch.cuda.ExternalStream(stream, device=self.device) if stream
+                   else torch.cuda.default_stream(self._index))
+            with torch.cuda.stream(own):      # memory of the stream that uses it, which orders its reuse
+                if torch.cuda.is_current_stream_capturing():
+                    _bad(fn, "no workspace of this size on the capturing stream yet: make the call once on it "
+                             "before the capture, or pass workspace", xgr.XGR_ERR_STATE)
+                if ws is not None:
+                    self._old.append(ws[0])
+                    need = max(need, 2 * ws[1])
+                t = torch.empty(need, dtype=torch.uint8, device=self.device)
             ws = self._ws[stream] = (t, need, t.data_ptr())
         return ws
 
@@ -240,9 +247,11 @@ class PagedCache:
         xgr.xgr_cache_compact(self._c, rows, d_table, d_used, d_ws, size, self._d_status, st)
 
     def device_status(self) -> int:
-        """Waits for the cache's device, returns the status word's bits (XGR_DEV_*) and clears them."""
+        """Waits for the cache's device, returns the status word's bits (XGR_DEV_*) and clears them.  (Bits of calls
+        that another thread makes meanwhile stay, unless they are the same.)"""
         self._torch.cuda.synchronize(self.device)
         code = int(self._status.item())
         if code:
-            self._status.zero_()
+            self._status.bitwise_and_(~code)
+            self._torch.cuda.current_stream(self._index).synchronize()
         return code

@@ -169,8 +169,11 @@ xgr_status xgr_cache_store(const xgr_cache *cache, const xgr_cache_rows *rows, c
  * so, and XGR_DEV_CAPACITY is set.  A parent outside [-1, n_rows) is taken for
  * -1 (XGR_DEV_INDEX).
  * d_table_out int32 [n_out][max_pages] and d_len_out [n_out] must not overlap
- * the arrays read.  The cache's pages that `rows` holds are not changed, so a
- * step can be taken back by going on from `rows`. */
+ * the arrays read.  Pages of rows without children are free in this very call:
+ * it may copy into them and hand them out, and a partly filled page that a row
+ * kept is written by that row's next store.  So `rows` is not to be gone on from
+ * afterwards.  A row to come back to is kept: its own parent, listed before its
+ * other children (who then get the copies), and not stored into. */
 xgr_status xgr_cache_fork_bytes(const xgr_cache *cache, int32_t n_rows, int32_t n_out,
                                 size_t *bytes);
 xgr_status xgr_cache_fork(const xgr_cache *cache, const xgr_cache_rows *rows, int32_t n_out,

@@ -215,7 +215,8 @@ class PagedCache:
 
     def fork(self, table, length, parent, n_new, table_out, len_out, *, stream=None, workspace=None):
         """The rows of the next step from their parents (-1: none), with pages for n_new[r] more
-        tokens (None: none).  See xgr_cache_fork."""
+        tokens (None: none).  Pages of rows without children are free in this very call: a row to
+        come back to is kept as its own parent, before its other children.  See xgr_cache_fork."""
         self._run(self._fork, table, length, parent, n_new, table_out, len_out, stream, workspace)
 
     def _fork(self, table, length, parent, n_new, table_out, len_out, stream, workspace):

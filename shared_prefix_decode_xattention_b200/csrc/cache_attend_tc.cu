@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
     } else if (warp > kIssueWarp) {
         // ------------------------------------------------------------ codes to operands
         const int cw = warp - kIssueWarp - 1;
-        // A block is the 512 bytes (kKeys keys) that a warp copies or converts at a time; the warps take every third.
+        // A block is the 512 bytes (kKeys keys) that a warp copies or converts at a time; warp cw takes every kConvWarps-th.
         // lane -> (key, 16-byte chunk) so that eight lanes' 16-byte writes meet no bank twice
         constexpr int kKeys = 512 / D, kBlocks = kChunk / kKeys, kTurns = (kBlocks + kConvWarps - 1) / kConvWarps;
         const int ck = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;

@@ -296,9 +296,10 @@ __device__ __forceinline__ float tanh_score(float y2) {   // y2 = 2 log2(e) y
 
 // The same for a pair of small arguments, |y| <= 1/2 (kTanhNear in y2's units):
 // tanh y = y P(y^2) with P of degree 4, a Chebyshev fit of tanh(y) / y on
-// [0, 1/4] whose relative error is 1.3e-8, below fp32's own.  Scores are mostly
-// this far inside their cap, and two MUFU operations a score (8 cycles of a
-// warp's scheduler each) cost more than the polynomial's packed FMAs.
+// [0, 1/4] whose relative error is 2.7e-8 (1.3e-7 with the roundings of its
+// evaluation in fp32).  Scores are mostly this far inside their cap, and two
+// MUFU operations a score (8 cycles of a warp's scheduler each) cost more than
+// the polynomial's packed FMAs.
 constexpr float kTanhNear = kLog2e;
 constexpr double tanh_coef(double c, int i) {   // c y^(2i + 1) as a factor of y2^(2i + 1)
     double f = c;

@@ -2,6 +2,8 @@
 import os
 import re
 
+import numpy as np
+
 CSRC = os.path.join(os.path.dirname(__file__), "..", "shared_prefix_decode_xattention_b200", "csrc")
 
 
@@ -32,3 +34,27 @@ def test_waits_of_whole_warps_have_one_verdict():
         assert last.group(1) in ("warp_wait", "__all_sync"), roles[last.start():at]
     lane = [m.group(0) for m in re.finditer(r"[^;{}]*\bmbar_wait\(", roles)]
     assert len(lane) == 3                           # (put to those votes: the scores' and the two operand buffers')
+
+
+def test_the_polynomial_for_small_capped_scores():
+    """The committed coefficients against tanh in 64 bits over their range, |y| <= 1/2, and evaluated as the kernels do
+    (in fp32, by y2 = 2 log2(e) y): within what the comment beside them states."""
+    path = os.path.join(CSRC, "cache_plan.cuh")
+    with open(path) as f:
+        raw = " ".join(f.read().replace("\n//", " ").split())
+    found = re.search(r"relative error is ([0-9.e-]+) \(([0-9.e-]+) with the roundings", raw)
+    assert found, "the comment states both errors"
+    fit, whole = float(found.group(1)), float(found.group(2))
+    c = [1.0] + [float.fromhex(x) for x in re.findall(r"tanh_coef\((-?0x[0-9a-f.]+p[-+]?\d+), \d\)", raw)]
+    assert len(c) == 5 and "constexpr float kTanhNear = kLog2e;" in raw
+    y = np.linspace(1e-4, 0.5, 400001)
+    err = np.abs(y * sum(k * y ** (2 * i) for i, k in enumerate(c)) / np.tanh(y) - 1).max()
+    assert 0.9 * fit <= err <= fit
+    unit = 2 * 1.4426950408889634
+    f32 = [np.float32(k / unit ** (2 * i + 1)) for i, k in enumerate(c)]
+    y2 = (y * unit).astype(np.float32)
+    u, r = y2 * y2, np.full_like(y2, f32[4])
+    for k in f32[3::-1]:
+        r = (r.astype(np.float64) * u + k).astype(np.float32)          # one rounding, as the kernels' fused operation
+    err = np.abs((r * y2).astype(np.float64) / np.tanh(y2.astype(np.float64) / unit) - 1).max()
+    assert 0.8 * whole <= err <= whole

@@ -13,7 +13,8 @@
  *   value = code * scale.  format XGR_CACHE_E4M3: codes are e4m3 (finite codes
  *   only: the two NaN codes are no valid contents).  XGR_CACHE_INT8: codes are
  *   two's complement.  xgr_cache_store writes powers of two as scales; the
- *   attention takes any finite non-negative scale.
+ *   attention takes any finite non-negative scale (softmax weights below 2^-100
+ *   of a query's largest may count as none, whatever their page's scale).
  *
  * Rows: row r (a sequence, a beam, or a request whose beams share a prompt)
  * owns line r of a page table, d_table int32 [n_rows][max_pages], and a length

@@ -158,11 +158,15 @@ __device__ __noinline__ float far_sum(uint32_t ts, const Scales &sc, float &far_
     return l;
 }
 
-// The result of such a segment in the usual form: O the mean, l = 1, relative to 2^M.
+// The result of such a segment in the usual form, O and l relative to the same 2^M.  Any M would do but for fp32's range:
+// with O the mean, l = 1, the parts of the row that others hold may be 2^-126 of it and still matter, if its own values are
+// that small.  So l is up to 2^60, as far as O is below the mean's usual size: then whatever is lost where parts meet weighs
+// less than 2^-100 of the row, or is less than 2^-40 of it beside larger values.
 template <int D>
 __device__ __noinline__ float2 far_mean(uint32_t to, float P, float M, float l) {
     tc::fence_after();
-    const float mean = l == 0.f ? 0.f : 1.f / l, f = M == -INFINITY ? 0.f : exp2f(M - P);
+    const float top = P + log2f(l), k = rintf(fminf(fmaxf(top - M, 0.f), 60.f));
+    const float mean = l == 0.f ? 0.f : 1.f / l, f = M == -INFINITY ? 0.f : exp2f(M - P + k);
 #pragma unroll 1
     for (int p = 0; p < D / 32; ++p) {
         float o[32];
@@ -174,7 +178,7 @@ __device__ __noinline__ float2 far_mean(uint32_t to, float P, float M, float l) 
         tc::st32(to + 32u * p, reinterpret_cast<const uint32_t *>(o));
     }
     tc::wait_st();
-    return make_float2(P + log2f(l), l == 0.f ? 0.f : 1.f);
+    return make_float2(top - k, l == 0.f ? 0.f : exp2f(k));
 }
 
 template <int D, int FMT>

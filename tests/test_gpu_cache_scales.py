@@ -166,3 +166,20 @@ def test_lse_of_long_heads_of_zeros(n):
     # (the sum of at most 40000 terms of one sign, in any order: each addition 2^-24 of it; hundreds in a chain)
     assert (lse.double() - want).abs().max().item() <= 2.0 ** -24 * (16 * want + 16 * score + 1000)
     assert not out.any()
+
+
+@pytest.mark.parametrize("n,G,L,extra", [(66, 5, 671, 20), (66, 1, 671, 20), (66, 1, 256, 1), (1, 4, 671, 20), (1, 4, 256, 1),
+                                         (9, 2, 671, 20)])
+def test_faint_pages_of_larger_scales(n, G, L, extra):
+    """The last pages hold the smallest scales and nearly all weight; the ones before, whose weights a bias brings to
+    2^-50 to 2^-90, have scales that make up for it.  In one block, and cut among blocks."""
+    rng = np.random.default_rng(n + L)
+    page, d = 128, 64
+    pages = -(-L // page)
+    cache = random_cache(rng, pages + 2, HKV, page, d, "int8")
+    table = random_table(rng, [L], page, pages + 2, extra)
+    last = 2 if L > 256 else 1
+    cache["vs"][table[0, : pages - last]] = 2.0 ** -50
+    cache["vs"][table[0, pages - last: pages]] = 2.0 ** -126
+    q, q64 = bf16(rng.standard_normal((n, HKV * G, d)))
+    check(cache, table, np.array([L]), np.array([0, n]), q, q64, dict(mask="full", slopes=[0.388] * (HKV * G)))

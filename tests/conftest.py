@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -27,6 +28,14 @@ def pytest_collection_modifyitems(config, items):
     for item in items:
         if "gpu" in item.keywords:
             item.add_marker(skip)
+
+
+@pytest.fixture(autouse=True)
+def _former_tests_graphs_are_gone(request):
+    """A CUDA graph that a former test left in a reference cycle (a caught exception's frame holds it) is destroyed when
+    the collector happens to run.  Within a later test's capture that ends the capture, so it runs before."""
+    if "gpu" in request.keywords:
+        gc.collect()
 
 
 @pytest.fixture(scope="session")

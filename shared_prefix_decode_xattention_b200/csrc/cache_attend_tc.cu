@@ -59,14 +59,14 @@ constexpr int kChunk = 128;                    // keys of a chunk
 constexpr int kRing = 4;                       // chunks whose scales are at hand
 constexpr uint32_t kTmemCols = 512;            // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512)
 constexpr float kZeroLogV = -150.f;            // log2 of a V scale of 0, as good as it: 448 * 2^-150 is 0 in bf16
-constexpr float kLowLogV = -60.f, kHighLogV = 30.f;   // scales for which l may be summed from the weights
-constexpr int kSick = 256, kFar = 512;         // of Scales::bad: a scale is NaN; the segment has met scales past those
+constexpr float kLowV = 0x1p-60f, kHighV = 0x1p30f;   // scales for which l may be summed from the weights
+constexpr int kFar = 256;                      // of Scales::bad: the segment has met scales past those, or that are NaN
 
 struct Scales {
     float2 k[8];                // by 16 keys: K scale, log2 V scale (0 where far)
     float iv[8];                // 1 / V scale (0 where far)
     float lv[8];                // log2 V scale
-    int bad;                    // bit g: group g lies in a page that is not there; kSick, kFar (all take the slow way)
+    int bad;                    // bit g: group g lies in a page that is not there; kFar (both take the slow way)
     int pad[3];
 };
 
@@ -79,8 +79,7 @@ struct Lay {
     static constexpr uint32_t v = 4 * kTile;
     static constexpr uint32_t raw = 6 * kTile;                // codes of the next K and V chunk (first the plan's scratch)
     static constexpr uint32_t sc = raw + 2 * kChunk * D;
-    static constexpr uint32_t p = sc + kRing * sizeof(Scales);   // [256] P of the rows of a segment past the scales' limits
-    static constexpr uint32_t unit = p + 1024;
+    static constexpr uint32_t unit = sc + kRing * sizeof(Scales);
     static constexpr uint32_t x = kTile;                      // [128] (M, l) of a narrow segment's second half: it has no
                                                               // second Q tile
     static constexpr uint32_t bar = unit + 64;
@@ -98,12 +97,11 @@ __device__ __forceinline__ uint32_t sw128(int row, int c) {
     return (uint32_t)(c >> 3) * Lay<D>::kHalf + (uint32_t)row * 128u + (uint32_t)(((c & 7) ^ (row & 7)) << 4);
 }
 
-// Bounded waits of a whole warp, with one verdict: a lane that gave up alone would leave the others in instructions that
-// take all 32.  (In the loops over chunks the vote stands beside slower work: right after the waits it cost 4 % of the
-// packed chunks' time, there 1.5 %.)
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-}
+// Softmax and conversion warps go on from a bounded wait whatever its verdict, and ask at the end of a segment whether one
+// gave up: a lane that left a loop alone would leave the others in instructions that take all 32.  Until then they work on
+// what is there; later waits end soon, as the flag is up, and nothing of the segment is written.  (A vote in the loops
+// over chunks instead: 512 beams 722 us, 696 without, ten passes after a pause.)
+__device__ __forceinline__ bool went_well(volatile int *abort) { return __all_sync(0xffffffffu, *abort == 0); }
 
 // A segment as every role sees it.
 struct Seg {
@@ -130,11 +128,18 @@ __device__ __forceinline__ Seg segment(const AttendArgs &a, const Parts &w, cons
     return s;
 }
 
-// A chunk past the scales' limits: its scores, log2 units without the V scales, into l (relative to 2^far_p from then on,
-// to 2^M before), and the V scales onto them.  Called by whole warps; not inlined, as with far_mean, since the loop around
-// it is rarely gone through and its registers are all taken (inlined: packed chunks 217 us, 214 so).
-__device__ __noinline__ float far_sum(uint32_t ts, const Scales &sc, float &far_p, float M, float l) {
-    float P = far_p == INFINITY ? M : far_p;
+// A row's state past the scales' limits, on the thread's stack: P (infinite before), and l relative to 2^P.
+struct Far {
+    float P, l;
+};
+
+// A chunk past the limits: its scores, log2 units without the V scales, into far.l (which takes over l, relative to 2^M, at
+// the first), and the V scales onto them.  Called by whole warps; not inlined, as with far_mean: the loop around it rarely
+// comes here and has no register to spare.
+__device__ __noinline__ void far_sum(uint32_t ts, const Scales &sc, Far &far, float M, float l) {
+    const bool begun = far.P != INFINITY;
+    float P = begun ? far.P : M;
+    if (begun) l = far.l;
 #pragma unroll 1
     for (int p = 0; p < 4; ++p) {
         float x[32], top = -INFINITY, sum = 0.f;
@@ -154,8 +159,7 @@ __device__ __noinline__ float far_sum(uint32_t ts, const Scales &sc, float &far_
         tc::st32(ts + 32u * p, reinterpret_cast<const uint32_t *>(x));
     }
     tc::wait_st();
-    far_p = fminf(P, 0x1.fffffep127f);   // (infinite stands for no such chunk, in every thread alike)
-    return l;
+    far = Far{fminf(P, 0x1.fffffep127f), l};   // (infinite stands for no such chunk, in every thread alike)
 }
 
 // The result of such a segment in the usual form, O and l relative to the same 2^M.  Any M would do but for fp32's range:
@@ -163,10 +167,11 @@ __device__ __noinline__ float far_sum(uint32_t ts, const Scales &sc, float &far_
 // that small.  So l is up to 2^60, as far as O is below the mean's usual size: then whatever is lost where parts meet weighs
 // less than 2^-100 of the row, or is less than 2^-40 of it beside larger values.
 template <int D>
-__device__ __noinline__ float2 far_mean(uint32_t to, float P, float M, float l) {
+__device__ __noinline__ void far_mean(uint32_t to, const Far &far, float &M, float &l) {
     tc::fence_after();
-    const float top = P + log2f(l), k = rintf(fminf(fmaxf(top - M, 0.f), 60.f));
-    const float mean = l == 0.f ? 0.f : 1.f / l, f = M == -INFINITY ? 0.f : exp2f(M - P + k);
+    const float all = far.l + l * 0.f;        // (l has met the NaNs of V scales)
+    const float top = far.P + log2f(all), k = rintf(fminf(fmaxf(top - M, 0.f), 60.f));
+    const float mean = all == 0.f ? 0.f : 1.f / all, f = M == -INFINITY ? 0.f : exp2f(M - far.P + k);
 #pragma unroll 1
     for (int p = 0; p < D / 32; ++p) {
         float o[32];
@@ -178,7 +183,8 @@ __device__ __noinline__ float2 far_mean(uint32_t to, float P, float M, float l) 
         tc::st32(to + 32u * p, reinterpret_cast<const uint32_t *>(o));
     }
     tc::wait_st();
-    return make_float2(top - k, l == 0.f ? 0.f : exp2f(k));
+    M = top - k;
+    l = all == 0.f ? 0.f : exp2f(k);
 }
 
 template <int D, int FMT>
@@ -249,8 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         int gc = 0;        // chunks of the segments before
         int cnt = 0;       // of them, this warpgroup's
         int nx = 0;        // narrow segments before
-        bool ok = true;
-        for (int left = share; ok && left > 0 && cur.r < c.n_rows;) {
+        for (int left = share; left > 0 && cur.r < c.n_rows;) {
             const Seg s = segment(a, units, cur, left);
             const int ia = cur.t * R + tr + (s.narrow ? 0 : 128 * h);
             const bool valid = ia < s.row.n * a.G;
@@ -317,14 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
             const int lo_max = __reduce_max_sync(0xffffffffu, valid ? vis.lo : 0);
             const int hi_min = __reduce_min_sync(0xffffffffu, vis.hi);
 
-            // l is relative to 2^M, as O is, and from a chunk marked kFar on to 2^P, P in shared memory (infinite before)
             float M = -INFINITY, l = 0.f;
-            float &far_p = *reinterpret_cast<float *>(base + L::p + 4 * (tid & 255));
-            far_p = INFINITY;
+            Far far{INFINITY, 0.f};   // (of a segment with chunks marked kFar)
             for (int i = 0; i < n; ++i) {
                 const int ch = s.chunk_of(h, i), gi = gc + ch;
-                const bool here = mbar_wait(bar(B_SC + gi % kRing), (gi / kRing) & 1, abort) &&
-                                  mbar_wait(bar(B_SFULL + h), (cnt + i) & 1, abort);
+                mbar_wait(bar(B_SC + gi % kRing), (gi / kRing) & 1, abort);
+                mbar_wait(bar(B_SFULL + h), (cnt + i) & 1, abort);
                 tc::fence_after();
                 const Scales &sc = ring[gi % kRing];
                 const int key0 = s.kb0 + ch * kChunk;
@@ -383,15 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                         tc::st32(ts + 32u * p, reinterpret_cast<const uint32_t *>(x));
                     }
                     tc::wait_st();
-                    if (sc.bad & kFar) l = far_sum(ts, sc, far_p, M, l);
+                    if (sc.bad & kFar) far_sum(ts, sc, far, M, l);
                 }
                 float x[128];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) tc::ld32(ts + 32u * p, x + 32 * p);
-                ok = __all_sync(0xffffffffu, here);   // (beside the loads; until here a warp that gave up reads what is there)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) tc::wait_ld_into(x + 32 * p);
-                if (!ok) break;
                 // t = fo.x f1 x + fo.y is a weight's exponent (x itself after the slow way)
                 const float2 *fo = slow ? unit : sc.k;
                 const float f1 = slow ? 1.f : f0;
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 if (raise) {
                     alpha = exp2_fast(M - top);
                     M = top;
-                    if (!(sc.bad & kFar)) l *= alpha;
+                    l *= alpha;
                 }
                 if (i > 0 && __any_sync(0xffffffffu, raise)) {   // O_h holds every product so far: S_h waited for them
 #pragma unroll 1
@@ -452,24 +453,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 mbar_arrive(bar(B_PFULL + h));
             }
             // ---- the segment's result
-            if (ok && n > 0) ok = warp_wait(bar(B_PVDONE + h), (cnt + n - 1) & 1, abort);
+            if (n > 0) mbar_wait(bar(B_PVDONE + h), (cnt + n - 1) & 1, abort);
             cnt += n;
             gc += s.chunks;
-            if (ok && far_p != INFINITY) {   // (of whole warps)
-                const float2 ml = far_mean<D>(to, far_p, M, l);
-                M = ml.x;
-                l = ml.y;
-            }
+            if (far.P != INFINITY) far_mean<D>(to, far, M, l);   // (of whole warps)
             bool fold = false;   // a narrow segment's second half is folded in
             float a0 = 1.f, a1 = 0.f;
-            if (ok && s.narrow && s.chunks > 1) {
+            if (s.narrow && s.chunks > 1) {
                 if (h == 1) {
                     tc::fence_before();
                     xch[tr] = make_float2(M, l);
                     mbar_arrive(bar(B_XCH));
-                    ok = warp_wait(bar(B_XDONE), nx & 1, abort);   // O_1 and xch are read
+                    mbar_wait(bar(B_XDONE), nx & 1, abort);   // O_1 and xch are read
                 } else {
-                    ok = warp_wait(bar(B_XCH), nx & 1, abort);
+                    mbar_wait(bar(B_XCH), nx & 1, abort);
                     const float2 y = xch[tr];
                     const float m = fmaxf(M, y.x), ref = m == -INFINITY ? 0.f : m;
                     a0 = exp2_fast(M - ref);
@@ -480,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 }
                 ++nx;
             }
-            if (!ok) break;
+            if (!went_well(abort)) break;
             if (!s.narrow || h == 0) {
                 tc::fence_after();
                 const bool all = cur.u == 0 && s.u1 == cur.units;
@@ -562,8 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
         const int ck = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
         const int kr = D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane >> 2;
         int gc = 0;
-        bool ok = true;
-        for (int left = share; ok && left > 0 && cur.r < c.n_rows;) {
+        for (int left = share; left > 0 && cur.r < c.n_rows;) {
             const Seg s = segment(a, units, cur, left);
             const int32_t *line = c.table + (int64_t)cur.r * c.max_pages;
             // Lane g of every warp holds group g % 8 of a chunk: its page (-2: no keys, -1: no such page), and where its
@@ -625,26 +621,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 const int gi = gc + ch, st = gi & 1;
                 const int ids2 = next;
                 next = ids_of(ch + 2);
-                if (gi >= 2) ok = mbar_wait(bar(B_KEMPTY + st), ((gi >> 1) - 1) & 1, abort);
+                if (gi >= 2) mbar_wait(bar(B_KEMPTY + st), ((gi >> 1) - 1) & 1, abort);
                 // (S of chunk gi - 2 is complete, so the softmax is done with the scales of chunk gi - 4)
                 if (cw == 0) {   // the chunk's scales
-                    float ks = 0.f, vs = 0.f;
+                    float ks = 0.f, vs = 1.f;
                     if (ids >= 0) {
                         const int64_t at_s = (int64_t)ids * c.Hkv + cur.g;
                         ks = clean_scale(c.ks[at_s]);
                         vs = clean_scale(c.vs[at_s]);
                     }
-                    const float lv = ids < 0 ? 0.f : vs != vs ? vs : fmaxf(log2f(vs), kZeroLogV);
-                    if (__any_sync(0xffffffffu, lv < kLowLogV || lv > kHighLogV)) met = kFar;
+                    if (__any_sync(0xffffffffu, !(vs >= kLowV && vs <= kHighV) || ks != ks)) met = kFar;
+                    const float lv = vs != vs ? vs : fmaxf(log2f(vs), kZeroLogV);
                     Scales &sc = ring[gi % kRing];
                     const uint32_t gone = __ballot_sync(0xffffffffu, ids == -1) & 255u;
-                    const uint32_t sick = __ballot_sync(0xffffffffu, vs != vs || ks != ks) & 255u;
                     if (lane < 8) {
                         sc.k[lane] = make_float2(ks, met ? 0.f : lv);
                         sc.iv[lane] = met ? 0.f : exp2f(-lv);
                         sc.lv[lane] = lv;
                     }
-                    if (lane == 0) sc.bad = (int)gone | (sick ? kSick : 0) | met;
+                    if (lane == 0) sc.bad = (int)gone | met;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_SC + gi % kRing));
                 }
@@ -653,15 +648,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_tc_kernel(AttendArgs
                 mbar_arrive(bar(B_KFULL + st));
                 block = block_of(ch + 1, ids2);
                 load(c.k, raw, ch + 1, block);
-                if (gi >= 2) ok = ok && mbar_wait(bar(B_VEMPTY + st), ((gi >> 1) - 1) & 1, abort);
+                if (gi >= 2) mbar_wait(bar(B_VEMPTY + st), ((gi >> 1) - 1) & 1, abort);
                 cp_async_wait_group<1>();
                 put(L::v + st * L::kTile, raw_v);
                 mbar_arrive(bar(B_VFULL + st));
                 load(c.v, raw_v, ch + 1, block);
                 ids = ids2;
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
             }
+            if (!went_well(abort)) break;
             gc += s.chunks;
             left -= s.u1 - cur.u;
             if (left > 0) plan_next(a, units, R, cur);

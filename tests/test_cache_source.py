@@ -23,17 +23,15 @@ def test_registers_are_exchanged_by_whole_warpgroups():
 
 
 def test_waits_of_whole_warps_have_one_verdict():
-    """Softmax and conversion warps go on to instructions of all 32 lanes: no lane leaves a loop on its own wait's result,
-    but all do by a vote on it."""
+    """Softmax and conversion warps go on to instructions of all 32 lanes: no lane acts on its own wait's result, all ask
+    for a vote on the flag that a wait which gave up has raised, at the end of a segment and before its result."""
     src = source("cache_attend_tc.cu")
     roles = src[src.index("if (warp < 8) {\n"):src.index("idS = tc::idesc")]
-    exits = [m.start() for m in re.finditer(r"if \(!ok\) break;", roles)]
-    assert len(exits) == 3                          # a chunk's softmax, a segment's end, a chunk's conversion
-    for at in exits:
-        last = list(re.finditer(r"ok = (\w+)\(", roles[:at]))[-1]
-        assert last.group(1) in ("warp_wait", "__all_sync"), roles[last.start():at]
-    lane = [m.group(0) for m in re.finditer(r"[^;{}]*\bmbar_wait\(", roles)]
-    assert len(lane) == 3                           # (put to those votes: the scores' and the two operand buffers')
+    assert len(re.findall(r"mbar_wait\(", roles)) == len(re.findall(r"(?<![=!&|(] )(?<!\()\bmbar_wait\([^;]*;", roles)) == 7
+    assert not re.search(r"(=|&&|\|\||!|if \()\s*mbar_wait\(", roles)
+    assert len(re.findall(r"if \(!went_well\(abort\)\) break;", roles)) == 2
+    assert roles.index("went_well") < roles.index("a.lse[oi]")
+    assert re.search(r"bool went_well\([^)]*\) \{ return __all_sync\(0xffffffffu, \*abort == 0\); \}", src)
 
 
 def test_the_polynomial_for_small_capped_scores():

@@ -50,7 +50,8 @@
  * order or past n_tokens anywhere, no row of an xgr_cache_attend has tokens, and
  * rows of an xgr_cache_store may be left out, each whole (XGR_DEV_INDEX in any
  * case).
- * XGR_DEV_TIMEOUT, as in xgr.h: a bounded wait inside xgr_cache_attend gave up.
+ * XGR_DEV_TIMEOUT, as in xgr.h: a bounded wait inside xgr_cache_attend gave up,
+ * and its results are not to be used.
  * The workspace of a call (d_ws, 256-byte aligned, at least the bytes its
  * _bytes function gives) needs no initial contents and holds nothing between
  * calls, so calls on one stream may share it; calls that may overlap on the
@@ -118,7 +119,7 @@ typedef struct {
  * and LSE -inf.  x_j = cap(scale * q.k_j) - slope * |pos - j|;
  * out = sum_j softmax(x)_j v_j; LSE = ln sum_j exp(x_j).
  * max_q: no row has more tokens than this (a row that does is skipped, and
- * XGR_DEV_CAPACITY set).  The beams of a request over its shared prompt are
+ * XGR_DEV_CAPACITY set; with 0 the call does nothing).  The beams of a request over its shared prompt are
  * one row with a token for each beam and XGR_ATTN_FULL, as many as there are;
  * slopes and window go by position under this mask too, where query i of n
  * stands at len - n + i (below 0 where n > len), not all beams at the end.
@@ -147,7 +148,7 @@ xgr_status xgr_cache_attend(const xgr_cache *cache, const xgr_cache_rows *rows, 
  * head gets NaN, whether in its K or its V; queries that see none are not
  * touched by it.
  * max_n: no row has more tokens than this (a row that does is skipped, and
- * XGR_DEV_CAPACITY set). */
+ * XGR_DEV_CAPACITY set; with 0 the call does nothing). */
 xgr_status xgr_cache_store(const xgr_cache *cache, const xgr_cache_rows *rows, const int32_t *d_cu,
                            int32_t n_tokens, int32_t max_n, const void *d_k, const void *d_v,
                            int64_t token_stride, int32_t *d_status, xgr_stream_t stream);

@@ -31,8 +31,9 @@
 // free of bank conflicts (perm and swz below).
 //
 // Measured: 64 rows of one token over 8.4k-10.2k e4m3 keys (1.23 GB, 32 / 8 heads,
-// D = 128): 214 us, 5.7 TB/s; capped 238 us.  Three rows of 9k-180k int8 keys with a
-// distance bias (0.33 GB): 86 us.  Some 780 instructions a warp and tile keep half
+// D = 128): 220 us, 5.6 TB/s; capped 246 us (ten passes after a pause; 266 where
+// hundreds run back to back).  Three rows of 9k-180k int8 keys with a distance bias
+// (0.33 GB): 85 us.  Some 780 instructions a warp and tile keep half
 // of the issue slots busy, so what is left is latency and issue, not bytes alone.
 #include <type_traits>
 
@@ -698,15 +699,15 @@ __global__ void __launch_bounds__(128) cache_tile_lo_kernel(AttendArgs a, int R,
 constexpr int kSmallCtas = 3 * kSms;         // 16-row tiles: three CTAs an SM
 constexpr int kWideCtas = 2 * kSms;          // 32-row tiles: two
 constexpr int kTcRows256 = 256;              // tcgen05 tiles: one
-// Fewest units a CTA takes: one row of 9300 keys takes 24.4 us with 4, 23.9 with 2, 27.7 with 8; four rows of 1000 to
-// 2000 keys 21.0, 21.4, 27.1.
+// Fewest units a CTA takes: one row of 9300 keys takes 24.1 us with 4, 24.9 with 2, 26.4 with 8; four rows of 1000 to
+// 2000 keys 20.7, 22.1, 25.7.
 constexpr int kMinUnits = 4;
 // A 256-row segment's rows and result cost about as much as three units of its keys, and as two where a cap makes keys
-// dearer.  7 and 12 packed chunks of 61 to 1000 tokens: without a cap 183 and 311 us with 3, 195 and 324 with 2 (7: 216
-// with 1); with a cap 212 and 358 with 2, 222 and 373 with 3 (7: 234 with 1).  Equal chunks differ by less than 2%.
+// dearer.  7 and 12 packed chunks of 61 to 1000 tokens: without a cap 188 and 318 us with 3, 201 and 333 with 2 (7: 224
+// with 1); with a cap 218 and 367 with 2, 224 and 378 with 3 (7: 241 with 1).  Equal chunks differ by less than 2%.
 constexpr int kTcLead = 3;
 constexpr int kTcLeadCapped = 2;
-// Rows of at most this many units are not cut and need no join: 200 rows of 300 to 800 keys 85 us, cut and joined 91.
+// Rows of at most this many units are not cut and need no join: 200 rows of 300 to 800 keys 86 us, cut and joined 93.
 constexpr int kWholeUnits = 8;
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -757,8 +758,9 @@ cudaError_t launch_cache_attend(const AttendArgs &in, cudaStream_t s) {
     const CacheArgs &c = a.c;
     a.whole = (int64_t)c.max_pages * c.page <= kWholeUnits * kUnitKeys;
     // 16 or 32 query rows a tile on mma.sync while no row has more; else 256 a tile on tcgen05.  Measured on 64 rows
-    // over 8.4k-10.2k keys, no cap: 16 query rows 224 us in 16-row tiles, 333 in 32-row ones; 32 query rows 344 us in
-    // 32-row tiles, 592 on tcgen05; 64 query rows 652 us in two 32-row tiles, 596 on tcgen05.
+    // over 8.4k-10.2k keys, no cap: 16 query rows 230 us in 16-row tiles, 327 in 32-row ones; 32 query rows 337 us in
+    // 32-row tiles, 588 on tcgen05; 64 query rows 639 us in two 32-row tiles, 593 on tcgen05.  (All rows of a call go one
+    // way: a chunk among single tokens takes them along to the 256-row tiles.)
     const int64_t most = (int64_t)a.max_q * a.G;
     const int R = most <= 16 ? 16 : most <= 32 ? 32 : kTcRows256;
     const int cap = R == 16 ? kSmallCtas : R == 32 ? kWideCtas : kSms;

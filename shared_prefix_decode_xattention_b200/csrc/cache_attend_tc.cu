@@ -35,12 +35,13 @@
 // scores may only be written once W V has read the weights over the old ones
 // (tensor memory is full: two S, two O of 128 columns); two tiles overlap their
 // chains.  Measured at 512 beams x 32 heads over 4096 keys, 16 requests (550
-// GFLOP; 1692 TFLOP/s of bf16 would take 325 us): 692 us, 795 TFLOP/s, 0.47 of the
-// measured bf16 rate (742 us where hundreds run back to back and the clock settles
-// lower); four conversion warps 696 us, three 870; weights through
-// shared memory instead, so that the next scores need not wait, 740 us (the
-// writes, and single operand buffers for want of room); the scores read in two
-// rolled passes 790 us; spills in the issuing warp (48 registers) 822 us.
+// GFLOP; 1692 TFLOP/s of bf16 would take 325 us): 713 us in ten passes after a
+// pause, 771 TFLOP/s, 0.46 of the measured bf16 rate; 759 where hundreds run back to
+// back and the clock settles lower.  Other forms, measured beside 692 us (without the
+// way for far V scales, which costs its code 2 to 3 %): four conversion warps 696 us,
+// three 870; weights through shared memory, so that the next scores need not wait, 740
+// (the writes, and single operand buffers for want of room); the scores read in two
+// rolled passes 790; spills in the issuing warp (48 registers) 822.
 // Every wait is bounded (XGR_DEV_TIMEOUT and an unwound CTA, no hang).
 #include "cache_codes.cuh"
 #include "cache_plan.cuh"

@@ -12,7 +12,7 @@
 // once.  W is set by the page's size, 64 values a thread: wide loads (two
 // 16-byte reads, one 16-byte write a thread and step) and enough of them in
 // flight.  Bound by HBM: 2 bytes in, 1 byte out a value; 590k tokens of 4 heads (1.83
-// GB) in 304 us, 6.0 TB/s.
+// GB) in 308 us, 5.9 TB/s, ten passes after a pause; 328 where hundreds run back to back.
 #include <cuda_fp8.h>
 
 #include "cache.cuh"
@@ -36,7 +36,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 // |x| <= 127, by the choice of the scale: adding 1.5 * 2^23 rounds to the nearest
 // whole number, ties to even, and leaves it in the low byte (the conversion
-// instruction runs at an eighth of the rate: 355 against 306 us for 590k tokens)
+// instruction runs at an eighth of the rate: 355 against 306 us for 590k tokens in short runs)
 __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
     auto q = [](float x) { return __float_as_uint(x + 12582912.f); };
     return __byte_perm(__byte_perm(q(a), q(b), 0x0040), __byte_perm(q(c), q(d), 0x0040), 0x5410);

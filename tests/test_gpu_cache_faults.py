@@ -100,3 +100,31 @@ def test_store_of_single_tokens_leaves_out_the_rows_at_fault():
     keep = [r for r in range(ROWS) if r not in (3, 4)]
     oc.store(cache, table[keep], lens[keep], np.arange(len(keep) + 1), k64[keep], k64[keep])
     same_cache(to_host(pc), cache)
+
+
+def test_calls_on_no_rows_and_no_tokens():
+    rng = np.random.default_rng(0)
+    cache = random_cache(rng, 12, 2, 16, 64, "int8")
+    pc = to_device(cache)
+    none, zero = torch.empty((0, 3), dtype=torch.int32, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    used = i32([7])
+    pc.compact(none, zero, torch.empty_like(none), used)
+    assert used.item() == 0
+    t2, l2 = i32(np.zeros((2, 3))), i32([5, 5])
+    pc.fork(none, zero, i32([-1, -1]), i32([4, 4]), t2, l2)            # rows without parents are empty, whatever they want
+    assert (t2 == -1).all() and l2.tolist() == [0, 0]
+    pc.fork(t2, l2, i32([0, 1]), i32([17, 0]), t3 := torch.empty_like(t2), l3 := torch.empty_like(l2))
+    assert t3.tolist() == [[0, 1, -1], [-1, -1, -1]] and l3.tolist() == [17, 0]
+    q = torch.ones((3, 4, 64), dtype=torch.bfloat16, device="cuda")
+    for mask, n in (("full", 1), ("causal", 1), ("full", 70)):
+        out, lse = torch.full_like(q, 7.0), torch.full((3, 4), 7.0, device="cuda")
+        pc.attend(t3, l3, i32([0, 0, 0]), q, out, lse, max_q=n, mask=mask)             # tokens of no row
+        assert (out == 7).all() and (lse == 7).all()
+        pc.attend(none, zero, i32([0]), q, out, lse, max_q=n, mask=mask)
+        assert (out == 7).all() and (lse == 7).all()
+        if mask == "full":                                                             # a row of no keys
+            pc.attend(t3, l3, i32([0, 0, 3]), q, out, lse, max_q=max(n, 3), mask=mask)
+            assert not out.any() and torch.isneginf(lse).all()
+    pc.store(t3, l3, i32([0, 0, 0]), q[:, :2], q[:, :2], max_n=3)
+    assert pc.device_status() == 0
+    same_cache(to_host(pc), cache)
